@@ -22,6 +22,12 @@ Entry points (same names as the C ABI):
   qmv_moe_swiglu                   MoE gate||up with the SwiGLU step fused
   qmv_moe_swiglu_xt                the same with fp32, fp16 or bf16 activations
   qmv_moe_combine                  MoE down with the router-weighted combine
+  qmv_group_plan                   items sorted by group: the plan of the grouped products
+  qmv_moe_grouped                  expert products grouped by expert, any number of tokens
+  qmv_moe_grouped_swiglu           gate||up with the SwiGLU step fused, grouped by expert
+  qmv_moe_weighted_sum             router-weighted sum over a token's slots
+  qmv_lora                         shared projection with a low-rank adapter per token
+  qmv_spec_verify                  drafted tokens against the target's probabilities
   qmv_dequant                      stored blocks -> fp32 (test/inspection aid)
   qmv_stream_read                  stream-read ceiling of the device (measurement aid)
   qmv_chain                        batch-1 matvec stages in one persistent launch
@@ -33,6 +39,8 @@ import os
 __all__ = ["QmvError", "qmv_q8_0", "qmv_q4_0", "qmv_q4_1", "qmv_q4_k", "qmv_q6_k", "qmv_matvec_path", "qmv_matvec_xt", "PATH_AUTO",
            "PATH_FMA", "PATH_MFMA", "X_F32", "X_F16", "X_BF16", "qmv_i8_requant", "qmv_i8_requant_lut",
            "qmv_moe", "qmv_moe_xt", "qmv_moe_swiglu", "qmv_moe_swiglu_xt", "qmv_moe_combine",
+           "GroupPlan", "qmv_group_plan", "qmv_moe_grouped", "qmv_moe_grouped_swiglu", "qmv_moe_weighted_sum",
+           "qmv_lora", "qmv_spec_verify",
            "qmv_dequant", "qmv_stream_read", "qmv_chain", "qmv_chain_noalloc", "ChainStage", "CHAIN_WORKSPACE_BYTES", "abi_version", "last_error",
            "library_path", "lib", "Q8_0", "Q4_0", "Q4_1", "Q4_K", "Q6_K", "FORMATS", "BLOCK_BYTES", "row_bytes"]
 
@@ -105,6 +113,24 @@ def _open():
         f.restype = i32
     L.qmv_moe_combine.argtypes = [ctypes.c_int, P, i64, i32, i64, i64, P, P, i32, i32, P, i64, i64, P, P]
     L.qmv_moe_combine.restype = i32
+    sz = ctypes.c_size_t
+    L.qmv_group_plan_bytes.argtypes = [i64, i32]
+    L.qmv_lora_workspace_bytes.argtypes = [i64, i32, i32]
+    L.qmv_spec_verify_workspace_bytes.argtypes = [i64, i32, i64]
+    for name in ("qmv_group_plan_bytes", "qmv_lora_workspace_bytes", "qmv_spec_verify_workspace_bytes"):
+        getattr(L, name).restype = sz
+    L.qmv_group_plan.argtypes = [P, i64, i32, P, sz, P]
+    L.qmv_group_plan.restype = i32
+    for name in ("qmv_moe_grouped", "qmv_moe_grouped_swiglu"):
+        f = getattr(L, name)
+        f.argtypes = [ctypes.c_int, P, i64, i32, i64, i64, P, i64, i32, P, i32, i64, i64, P, i32, P]
+        f.restype = i32
+    L.qmv_moe_weighted_sum.argtypes = [P, i32, P, i64, i32, i64, P, i32, P]
+    L.qmv_moe_weighted_sum.restype = i32
+    L.qmv_lora.argtypes = [ctypes.c_int, P, i64, i64, P, i32, i64, i64, P, P, i32, i32, i32, P, P, P, i64, P, sz, P]
+    L.qmv_lora.restype = i32
+    L.qmv_spec_verify.argtypes = [P, i32, i64, i64, P, i64, i64, P, P, P, P, i64, i32, i64, P, P, P, sz, P]
+    L.qmv_spec_verify.restype = i32
     L.qmv_dequant.argtypes = [ctypes.c_int, P, i64, i64, P, P]
     L.qmv_dequant.restype = i32
     L.qmv_stream_read.argtypes = [P, ctypes.c_size_t, P, ctypes.c_size_t, P]
@@ -425,6 +451,214 @@ def qmv_moe(fmt, W_experts, expert_stride_bytes, n_experts, n_rows, n_cols, expe
                         expert_ids.data_ptr(), B, T, x.data_ptr(), st_tok, st_slot, y.data_ptr(),
                         _stream(stream)))
     return y
+
+
+class GroupPlan:
+    """Items sorted by group (qmv_group_plan): the device buffer and its sizes."""
+    __slots__ = ("buffer", "n_items", "n_groups")
+
+    def __init__(self, buffer, n_items, n_groups):
+        self.buffer, self.n_items, self.n_groups = buffer, n_items, n_groups
+
+
+def _scratch(buf, name, need, like, stream):
+    """A caller's uint8 buffer of at least `need` bytes, or a new one, kept
+    from reuse until a stream other than the current one is done with it."""
+    torch = _torch()
+    if buf is None:
+        buf = torch.empty(max(need, 16), dtype=torch.uint8, device=like.device)
+        if stream is not None:
+            buf.record_stream(stream)
+        return buf
+    _dev(buf, name, torch.uint8)
+    if not buf.is_contiguous() or buf.numel() < need:
+        raise ValueError(f"{name} must be contiguous and hold {need} bytes")
+    return buf
+
+
+def _type_of(t, name):
+    torch = _torch()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    xt = _x_types(torch).get(t.dtype)
+    if xt is None:
+        raise ValueError(f"{name} must be float32, float16 or bfloat16 (got {t.dtype})")
+    _dev(t, name, t.dtype)
+    return xt
+
+
+def qmv_group_plan(group_ids, n_groups, plan=None, stream=None):
+    """Sorts the items of group_ids (int32, any shape, contiguous, on the GPU)
+    by group and returns the GroupPlan that the grouped products take.  plan:
+    a uint8 GPU tensor to build it in (its size: the library's
+    qmv_group_plan_bytes), or None for a new one."""
+    torch = _torch()
+    _dev(group_ids, "group_ids", torch.int32)
+    if not group_ids.is_contiguous():
+        raise ValueError("group_ids must be contiguous")
+    n = group_ids.numel()
+    buf = _scratch(plan, "plan", _lib.qmv_group_plan_bytes(n, n_groups), group_ids, stream)
+    _check(_lib.qmv_group_plan(group_ids.data_ptr(), n, n_groups, buf.data_ptr(), buf.numel(), _stream(stream)))
+    return GroupPlan(buf, n, n_groups)
+
+
+def _grouped(cfn, fmt, W, stride, E, rows, matrix_rows, cols, plan, top_k, x, out, name, dtype, stream):
+    torch = _torch()
+    f = _fmt(fmt)
+    _dev(W, "W_experts", torch.uint8)
+    if not W.is_contiguous() or W.numel() < (E - 1) * stride + matrix_rows * row_bytes(f, cols):
+        raise ValueError("W_experts must be contiguous and hold n_experts expert matrices")
+    xt = _type_of(x, "x")
+    if x.dim() == 2 and x.shape[1] == cols and x.stride(1) == 1:
+        st_tok, st_slot = x.stride(0), 0
+    elif x.dim() == 3 and tuple(x.shape[1:]) == (top_k, cols) and x.stride(2) == 1:
+        st_tok, st_slot = x.stride(0), x.stride(1)
+    else:
+        raise ValueError("x must be [tokens, K] or [tokens, top_k, K] with K = n_cols and unit inner stride")
+    T = x.shape[0]
+    if not isinstance(plan, GroupPlan) or plan.n_items != T * top_k or plan.n_groups != E:
+        raise ValueError(f"plan must be qmv_group_plan's of {T * top_k} items and {E} groups")
+    if out is None:
+        out = torch.empty((T, top_k, rows), dtype=dtype or torch.float32, device=x.device)
+    ot = _type_of(out, name)
+    if tuple(out.shape) != (T, top_k, rows) or not out.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous [tokens, top_k, {rows}] tensor")
+    _check(cfn(f, W.data_ptr(), stride, E, rows, cols, plan.buffer.data_ptr(), T, top_k, x.data_ptr(), xt, st_tok,
+               st_slot, out.data_ptr(), ot, _stream(stream)))
+    return out
+
+
+def qmv_moe_grouped(fmt, W_experts, expert_stride_bytes, n_experts, n_rows, n_cols, plan, top_k, x, y=None,
+                    y_dtype=None, stream=None):
+    """Expert products for any number of tokens, grouped by expert.
+
+    plan: qmv_group_plan(expert_ids, n_experts) of the int32 [tokens, top_k]
+    expert ids.  x: float32, float16 or bfloat16, [tokens, K] or [tokens,
+    top_k, K].  Returns y [tokens, top_k, n_rows] of y_dtype (float32 by
+    default)."""
+    return _grouped(_lib.qmv_moe_grouped, fmt, W_experts, expert_stride_bytes, n_experts, n_rows, n_rows, n_cols, plan,
+                    top_k, x, y, "y", y_dtype, stream)
+
+
+def qmv_moe_grouped_swiglu(fmt, W_experts, expert_stride_bytes, n_experts, n_ff, n_cols, plan, top_k, x, h=None,
+                           h_dtype=None, stream=None):
+    """qmv_moe_grouped over experts of 2*n_ff rows (gate, then up): returns
+    h [tokens, top_k, n_ff] = SiLU(gate x) * (up x) of h_dtype."""
+    return _grouped(_lib.qmv_moe_grouped_swiglu, fmt, W_experts, expert_stride_bytes, n_experts, n_ff, 2 * n_ff,
+                    n_cols, plan, top_k, x, h, "h", h_dtype, stream)
+
+
+def qmv_moe_weighted_sum(y, weights, out=None, out_dtype=None, stream=None):
+    """out [tokens, n_rows] = sum over the slots of weights[t, s] * y[t, s];
+    y float32, float16 or bfloat16 [tokens, top_k, n_rows], weights float32
+    [tokens, top_k]."""
+    torch = _torch()
+    yt = _type_of(y, "y")
+    _dev(weights, "weights", torch.float32)
+    if y.dim() != 3 or not y.is_contiguous():
+        raise ValueError("y must be a contiguous [tokens, top_k, n_rows] tensor")
+    T, S, N = y.shape
+    if tuple(weights.shape) != (T, S) or not weights.is_contiguous():
+        raise ValueError("weights must be a contiguous [tokens, top_k] tensor")
+    if out is None:
+        out = torch.empty((T, N), dtype=out_dtype or torch.float32, device=y.device)
+    ot = _type_of(out, "out")
+    if tuple(out.shape) != (T, N) or not out.is_contiguous():
+        raise ValueError("out must be a contiguous [tokens, n_rows] tensor")
+    _check(_lib.qmv_moe_weighted_sum(y.data_ptr(), yt, weights.data_ptr(), T, S, N, out.data_ptr(), ot,
+                                     _stream(stream)))
+    return out
+
+
+def qmv_lora(fmt, W, n_rows, n_cols, x, A, B, scales, adapter_ids, y=None, workspace=None, stream=None):
+    """y[t] = DEQ(W) @ x[t] + scales[a] * B[a] @ (A[a] @ x[t]) with a =
+    adapter_ids[t] (-1: the base alone).
+
+    x: float32, float16 or bfloat16 [tokens, K]; A [adapters, rank, K] and B
+    [adapters, n_rows, rank] of one of these types; scales float32
+    [adapters]; adapter_ids int32 [tokens].  y is float32 [tokens, n_rows].
+    workspace: a uint8 GPU tensor of the library's qmv_lora_workspace_bytes,
+    or None for a new one."""
+    torch = _torch()
+    f = _fmt(fmt)
+    _dev(W, "W", torch.uint8)
+    need = n_rows * row_bytes(f, n_cols)
+    if W.numel() < need or not W.is_contiguous():
+        raise ValueError(f"W must be contiguous and hold {need} bytes")
+    xt = _type_of(x, "x")
+    if x.dim() != 2:
+        raise ValueError("x must be [tokens, K]")
+    x2, T, ldx = _rows2d(x, "x", n_cols)
+    at = _type_of(A, "A")
+    _dev(B, "B", A.dtype)
+    if A.dim() != 3 or A.shape[2] != n_cols or not A.is_contiguous():
+        raise ValueError("A must be a contiguous [adapters, rank, K] tensor")
+    G, R = A.shape[0], A.shape[1]
+    if tuple(B.shape) != (G, n_rows, R) or not B.is_contiguous():
+        raise ValueError(f"B must be a contiguous [{G}, {n_rows}, {R}] tensor")
+    _dev(scales, "scales", torch.float32)
+    _dev(adapter_ids, "adapter_ids", torch.int32)
+    if tuple(scales.shape) != (G,) or not scales.is_contiguous():
+        raise ValueError("scales must be a contiguous [adapters] tensor")
+    if tuple(adapter_ids.shape) != (T,) or not adapter_ids.is_contiguous():
+        raise ValueError("adapter_ids must be a contiguous [tokens] tensor")
+    if y is None:
+        y = torch.empty((T, n_rows), dtype=torch.float32, device=x.device)
+    _dev(y, "y", torch.float32)
+    y2, Ty, ldy = _rows2d(y, "y", n_rows)
+    if Ty != T:
+        raise ValueError("y must have as many rows as x")
+    ws = _scratch(workspace, "workspace", _lib.qmv_lora_workspace_bytes(T, R, G), x, stream)
+    _check(_lib.qmv_lora(f, W.data_ptr(), n_rows, n_cols, x2.data_ptr(), xt, ldx, T, A.data_ptr(), B.data_ptr(), at, G,
+                         R, scales.data_ptr(), adapter_ids.data_ptr(), y2.data_ptr(), ldy, ws.data_ptr(), ws.numel(),
+                         _stream(stream)))
+    return y
+
+
+def qmv_spec_verify(logits, draft_probs, draft_tokens, n_draft, u_accept, u_last, tokens=None, n_kept=None,
+                    workspace=None, stream=None):
+    """Keeps drafted tokens while u q(x) < p(x), p the softmax of the target's
+    logits, and draws one more token (see qmv.h).
+
+    logits: float32, float16 or bfloat16 [requests, drafts + 1, vocab];
+    draft_probs: float32 [requests, drafts, vocab], or None (each draft's
+    probability all on its token); draft_tokens int32 [requests, drafts];
+    n_draft int32 [requests]; u_accept float32 [requests, drafts]; u_last
+    float32 [requests].  Returns (tokens int32 [requests, drafts + 1],
+    n_kept int32 [requests])."""
+    torch = _torch()
+    lt = _type_of(logits, "logits")
+    if logits.dim() != 3 or logits.stride(2) != 1:
+        raise ValueError("logits must be [requests, drafts + 1, vocab] with unit inner stride")
+    Q, D1, V = logits.shape
+    D = D1 - 1
+
+    def flat(t, name, dtype, shape):
+        _dev(t, name, dtype)
+        if tuple(t.shape) != shape or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous {list(shape)} tensor")
+        return t.data_ptr()
+    qp, qr, ql = None, 0, 0
+    if draft_probs is not None:
+        _dev(draft_probs, "draft_probs", torch.float32)
+        if tuple(draft_probs.shape) != (Q, D, V) or draft_probs.stride(2) != 1:
+            raise ValueError("draft_probs must be [requests, drafts, vocab] with unit inner stride")
+        qp, qr, ql = draft_probs.data_ptr(), draft_probs.stride(0), draft_probs.stride(1)
+    if tokens is None:
+        tokens = torch.empty((Q, D + 1), dtype=torch.int32, device=logits.device)
+    if n_kept is None:
+        n_kept = torch.empty((Q,), dtype=torch.int32, device=logits.device)
+    ws = _scratch(workspace, "workspace", _lib.qmv_spec_verify_workspace_bytes(Q, D, V), logits,
+                  stream)
+    _check(_lib.qmv_spec_verify(logits.data_ptr(), lt, logits.stride(0), logits.stride(1), qp, qr, ql,
+                                flat(draft_tokens, "draft_tokens", torch.int32, (Q, D)),
+                                flat(n_draft, "n_draft", torch.int32, (Q,)),
+                                flat(u_accept, "u_accept", torch.float32, (Q, D)),
+                                flat(u_last, "u_last", torch.float32, (Q,)), Q, D, V,
+                                flat(tokens, "tokens", torch.int32, (Q, D + 1)),
+                                flat(n_kept, "n_kept", torch.int32, (Q,)), ws.data_ptr(), ws.numel(),
+                                _stream(stream)))
+    return tokens, n_kept
 
 
 def qmv_dequant(fmt, W, n_rows, n_cols, out=None, stream=None):

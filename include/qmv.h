@@ -458,6 +458,132 @@ int32_t qmv_chain(qmv_fmt fmt, const qmv_chain_stage* stages, int32_t n_stages, 
 int32_t qmv_chain_noalloc(qmv_fmt fmt, const qmv_chain_stage* stages, int32_t n_stages, void* stream);
 
 /*
+ * Products grouped by expert, for any number of tokens (prompts, many
+ * requests at once; qmv_moe takes up to 8).
+ *
+ * qmv_group_plan sorts items by group: item i belongs to group group_ids[i].
+ * For MoE the items are the (token, slot) pairs, i = token * top_k + slot,
+ * and the groups the experts; one plan serves every product of the same
+ * routing (gate||up and down).  The sort is stable, so the plan's bytes are
+ * the same for the same ids.  An id outside [0, n_groups) is no error here:
+ * the products write quiet NaN for its item.
+ *   group_ids  int32 [n_items], device memory.
+ *   n_items    1..2^24;  n_groups  1..1024.
+ *   plan       device memory of >= qmv_group_plan_bytes(n_items, n_groups)
+ *              bytes, 16-byte aligned; its contents are the library's.
+ * qmv_group_plan_bytes is a host function (0 for sizes out of range).
+ * Errors: QMV_EINVAL, QMV_EALIGN, QMV_EHIP.
+ */
+size_t qmv_group_plan_bytes(int64_t n_items, int32_t n_groups);
+int32_t qmv_group_plan(const int32_t* group_ids, int64_t n_items, int32_t n_groups, void* plan, size_t plan_bytes,
+                       void* stream);
+
+/*
+ * y[(t*top_k + s)*n_rows + i] = sum_j DEQ(W_e)[i][j] * x_{t,s}[j], e the
+ * expert of item t*top_k + s in `plan`, W_e and x_{t,s} as in qmv_moe.
+ *   plan      a plan of n_tokens * top_k items and n_experts groups (where
+ *             its sizes are others, nothing is written).
+ *   n_tokens * top_k  1..2^24 with top_k 1..1024;  n_experts 1..1024.
+ *   expert_stride_bytes  >= an expert's bytes; a multiple of 2 (Q4_1: 4,
+ *             Q4_K: 16); W_experts aligned as for the matvec.
+ *   n_cols    a multiple of the format's unit (32, or 256 for Q4_K and Q6_K).
+ *   x         x_type elements, aligned to the element size; 16-byte aligned
+ *             with strides of a multiple of 16 bytes it is read in 16-byte
+ *             pieces.  x_stride_token >= n_cols (where n_tokens > 1),
+ *             x_stride_slot 0 or >= n_cols.
+ *   y         y_type (QMV_X_F32, QMV_X_F16, QMV_X_BF16) [n_tokens][top_k]
+ *             [n_rows], each output rounded once from fp32.
+ * Codes are exact in the matrix cores' types, 16-bit activations too, and
+ * fp32 activations are split into three bf16 pieces (24 bits); sums and
+ * scales are fp32: the accuracy contract holds as for the matvec.  An item's
+ * outputs do not depend on the other items.
+ * Errors: QMV_EINVAL, QMV_EALIGN, QMV_EUNSUPPORTED (unknown fmt), QMV_EHIP.
+ */
+int32_t qmv_moe_grouped(qmv_fmt fmt, const void* W_experts, int64_t expert_stride_bytes, int32_t n_experts,
+                        int64_t n_rows, int64_t n_cols, const void* plan, int64_t n_tokens, int32_t top_k,
+                        const void* x, int32_t x_type, int64_t x_stride_token, int64_t x_stride_slot,
+                        void* y, int32_t y_type, void* stream);
+
+/*
+ * qmv_moe_grouped over experts of 2*n_ff rows (gate, then up) with
+ * h = SiLU(gate) * up, as in qmv_moe_swiglu; h is h_type [n_tokens][top_k]
+ * [n_ff], SiLU and the product in fp32, rounded once.
+ */
+int32_t qmv_moe_grouped_swiglu(qmv_fmt fmt, const void* W_experts, int64_t expert_stride_bytes, int32_t n_experts,
+                               int64_t n_ff, int64_t n_cols, const void* plan, int64_t n_tokens, int32_t top_k,
+                               const void* x, int32_t x_type, int64_t x_stride_token, int64_t x_stride_slot,
+                               void* h, int32_t h_type, void* stream);
+
+/*
+ * out[t*n_rows + i] = sum_s weights[t*top_k + s] * y[(t*top_k + s)*n_rows + i]:
+ * the router-weighted combine of qmv_moe_grouped's outputs, an fp32 fused
+ * multiply-add chain in slot order, rounded once to out_type.
+ * Errors: QMV_EINVAL, QMV_EALIGN, QMV_EHIP.
+ */
+int32_t qmv_moe_weighted_sum(const void* y, int32_t y_type, const float* weights, int64_t n_tokens, int32_t top_k,
+                             int64_t n_rows, void* out, int32_t out_type, void* stream);
+
+/*
+ * A projection of shared quantized weights with a low-rank adapter per
+ * token, for the tokens of many requests at once ([NST] QLoRA Lemma: the
+ * frozen DEQ(W) beside a 16-bit adapter):
+ *   y[t] = DEQ(W) x[t] + scales[a] * B_a (A_a x[t]),  a = adapter_ids[t].
+ * a = -1: the base alone.  Any other id outside [0, n_adapters): the token's
+ * outputs are quiet NaN.
+ *   W, n_rows, n_cols, x, x_type, ldx, y, ldy  as qmv_matvec_xt, with n_rows
+ *            up to 2^24, n_cols up to 35424 and 1..2^20 tokens.
+ *   A        a_type (QMV_X_F32, QMV_X_F16, QMV_X_BF16) [n_adapters][rank][n_cols]
+ *   B        a_type [n_adapters][n_rows][rank]
+ *   rank     1..128 (smaller adapters padded with zeros);  n_adapters 1..1024.
+ *   scales   fp32 [n_adapters];  adapter_ids  int32 [n_tokens], device memory.
+ *   workspace  device memory of >= qmv_lora_workspace_bytes(...) bytes,
+ *            16-byte aligned; any contents; calls that share one must not
+ *            run concurrently.
+ * The base is the matvec's result up to 8 tokens; the adapters' products and
+ * sums are fp32.  A token's outputs do not depend on other tokens' adapters.
+ * Errors: QMV_EINVAL, QMV_EALIGN, QMV_EUNSUPPORTED (unknown fmt), QMV_EHIP.
+ */
+size_t qmv_lora_workspace_bytes(int64_t n_tokens, int32_t rank, int32_t n_adapters);
+int32_t qmv_lora(qmv_fmt fmt, const void* W, int64_t n_rows, int64_t n_cols, const void* x, int32_t x_type,
+                 int64_t ldx, int64_t n_tokens, const void* A, const void* B, int32_t a_type, int32_t n_adapters,
+                 int32_t rank, const float* scales, const int32_t* adapter_ids, float* y, int64_t ldy,
+                 void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Verification of drafted tokens against the target's probabilities, from
+ * given random numbers: the step after the lm_head at widths 2..8, for many
+ * requests.  Request r has n = n_draft[r] drafted tokens (clamped to 0..max_drafts)
+ * and logits rows 0..n; p_i = softmax(row i), q_i the draft's probabilities
+ * at i (null draft_probs: all on the drafted token).  Tokens are kept in
+ * order while u_accept[r][i] * q_i(x_i) < p_i(x_i); at the first rejected, i,
+ * one token is drawn from max(p_i - q_i, 0) (from p_i where that is 0
+ * throughout), and where all are kept, one from p_n: the first token whose
+ * running sum of weights is greater than u_last[r] times their total.
+ *   logits     logits_type [n_requests][max_drafts + 1][vocab], strides in
+ *              elements, each >= vocab.  -inf is a probability of 0.  A row
+ *              of -inf throughout, or with NaN or +inf, keeps and draws
+ *              nothing.
+ *   draft_probs  fp32 [n_requests][max_drafts][vocab], strides as above; or null.
+ *   draft_tokens int32 [n_requests][max_drafts]; one outside [0, vocab) is
+ *              rejected.
+ *   u_accept   fp32 [n_requests][max_drafts] in [0, 1);  u_last fp32 [n_requests].
+ *   tokens     int32 [n_requests][max_drafts + 1]: the kept tokens, the drawn
+ *              one (-1: none), then -1.
+ *   n_kept     int32 [n_requests].
+ *   n_requests 1..65535, max_drafts 1..64, vocab 1..2^22.
+ *   workspace  device memory of >= qmv_spec_verify_workspace_bytes(...)
+ *              bytes, 16-byte aligned; any contents.
+ * Exponentials and sums are fp64.  Errors: QMV_EINVAL, QMV_EALIGN, QMV_EHIP.
+ */
+size_t qmv_spec_verify_workspace_bytes(int64_t n_requests, int32_t max_drafts, int64_t vocab);
+int32_t qmv_spec_verify(const void* logits, int32_t logits_type, int64_t logits_stride_request,
+                        int64_t logits_stride_row, const float* draft_probs, int64_t probs_stride_request,
+                        int64_t probs_stride_row, const int32_t* draft_tokens, const int32_t* n_draft,
+                        const float* u_accept, const float* u_last, int64_t n_requests, int32_t max_drafts,
+                        int64_t vocab, int32_t* tokens, int32_t* n_kept, void* workspace, size_t workspace_bytes,
+                        void* stream);
+
+/*
  * Dequantize a whole matrix to fp32: out[i][j] = DEQ(W)[i][j], exactly (every
  * Q8_0/Q4_0 value and every Q4_1 value d*c + m whose bits span <= 24 is
  * representable in fp32; otherwise it is rounded to nearest even; a Q4_K
