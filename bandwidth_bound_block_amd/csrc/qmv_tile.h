@@ -35,6 +35,12 @@ typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
+// Calls fn(std::integral_constant<int, J>{}) for J = 0..N-1 in order.
+template <class Fn, int... Js>
+__device__ __forceinline__ void static_for(std::integer_sequence<int, Js...>, Fn&& fn) {
+    (fn(std::integral_constant<int, Js>{}), ...);
+}
+
 __device__ __forceinline__ uint32_t fbits(float f) { return __builtin_bit_cast(uint32_t, f); }
 
 // --------------------------------------------------------------- operands
@@ -284,13 +290,27 @@ template <> struct X8<float> {
     }
 };
 
+// mu (SIDE 0) or a block sum of x (SIDE 1) as eight bf16 of an MFMA operand:
+// three pieces each, h, m and l, in six places whose products add up to
+// mu * sum but for terms of 2^-24 of it: hh, mh, hm, mm, lh, hl.
+template <int SIDE>
+__device__ __forceinline__ u32x4 min_operand(float v) {
+    const uint32_t h = __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{v, 0.f}, bf16x2));
+    float r = v - __builtin_bit_cast(float, h << 16);
+    const uint32_t m = __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{r, 0.f}, bf16x2));
+    r -= __builtin_bit_cast(float, m << 16);
+    const uint32_t l = __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{r, 0.f}, bf16x2));
+    return SIDE == 0 ? u32x4{h | (m << 16), h | (m << 16), l | (h << 16), 0}
+                     : u32x4{h | (h << 16), m | (m << 16), h | (l << 16), 0};
+}
+
 // --------------------------------------------------------------- the kernel
 struct TileDev {
     const uint8_t* W;
     int64_t estride;
     int rows, nb, row_tiles;
     const int32_t* plan;
-    int n_items, n_groups, top_k;
+    int n_items, n_groups, top_k, plan_tile;
     const void* x;
     int64_t xs_tok, xs_slot;
     void* y;
@@ -310,55 +330,83 @@ __device__ __forceinline__ void store_y(void* y, int y_type, int64_t at, float v
     }
 }
 
-constexpr int kTileRows = 128;    // weight rows of a workgroup's tile
 constexpr int kTileBlks = 2;      // 32-weight blocks of a step
 constexpr int kTilePitch = 64 * kTileBlks + 16;   // bytes of a staged row: an odd number of 16-byte units, so 8 rows hit distinct banks
+constexpr int kXcds = 8;          // workgroups go to the XCDs in turn
+constexpr int kTokGroup = 8;      // token tiles that an XCD takes together
 
+// A workgroup of kNW waves: kTM weight rows (one block of one row per thread
+// and step) by TN tokens; a wave takes 32 kRS rows by 32 kTS tokens.
 template <class F, class XT, int TN>
 struct TileShape {
     static constexpr int kP = XOp<XT>::kPieces;
-    static constexpr int kWr = TN >= 128 ? 2 : 4;                   // waves along the rows
-    static constexpr int kWt = 4 / kWr;                             // waves along the tokens
-    static constexpr int kRS = kTileRows / kWr / 32;                // 32-row pieces of a wave
-    static constexpr int kTS = TN / kWt / 32;                       // 32-token pieces of a wave
-    static constexpr int kW = kTileRows * kTilePitch;
+    static constexpr int kNW = TN == 64 ? 8 : 4;
+    static constexpr int kNT = 64 * kNW;
+    static constexpr int kTM = kNT / kTileBlks;
+    static constexpr int kWt = TN == 32 ? 1 : 2;                    // waves along the tokens
+    static constexpr int kWr = kNW / kWt;                           // waves along the rows
+    static constexpr int kRS = kTM / kWr / 32;
+    static constexpr int kTS = TN / kWt / 32;
+    static constexpr int kXL = TN * 8 / kNT;                        // 8-column pieces of x per thread and step 
+    static constexpr int kW = kTM * kTilePitch;
     static constexpr int kX = kP * TN * kTilePitch;
-    static constexpr int kS = kTileBlks * Unit<F>::kSub * kTileRows * 4;
-    static constexpr int kM = Unit<F>::kSums ? kTileBlks * (kTileRows + TN) * 4 : 0;
+    static constexpr int kS = kTileBlks * Unit<F>::kSub * kTM * 4;
+    static constexpr int kM = Unit<F>::kSums ? kTileBlks * (kTM + TN) * 16 : 0;
     static constexpr int kBuf = kW + kX + kS + kM;
-    static constexpr int kOutPitch = kTileRows + 4;                 // floats
+    static constexpr int kOutPitch = kTM + 4;                       // floats
     static constexpr int kLds = 2 * kBuf > TN * kOutPitch * 4 ? 2 * kBuf : TN * kOutPitch * 4;
+    static_assert(kXL >= 1 && kRS >= 1 && kTS >= 1, "every thread stages");
 };
 
 template <class F, class XT, int TN>
-__global__ __launch_bounds__(256) void tile_kernel(const TileDev a) {
+__global__ __launch_bounds__((TN == 64 ? 512 : 256), 2) void tile_kernel(const TileDev a) {
     using S = TileShape<F, XT, TN>;
     using U = Unit<F>;
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
     __shared__ int s_item[TN];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int rt = blockIdx.x % a.row_tiles, tt = blockIdx.x / a.row_tiles;
-    const int out_rows = a.swiglu ? kTileRows / 2 : kTileRows;
-    const int row0 = rt * out_rows;
 
-    int group = 0, start = tt * TN, count = min(TN, a.n_items - start);
+    // Tiles in runs, one run to an XCD, and within it kTokGroup token tiles
+    // side by side down the rows: the tiles an XCD works on at one time
+    // share their weights and activations in its L2.
+    const int split = a.plan_tile / TN;      // workgroups along a plan's tile
+    int tok_tiles;
     if (a.plan) {
         // a plan of other items or groups than the call's is not followed
-        if (a.plan[0] != kPlanMagic || a.plan[1] != a.n_items || a.plan[2] != a.n_groups || a.plan[3] != TN) return;
-        if (tt >= a.plan[4]) return;
-        const int* t = a.plan + a.tiles_at + 4 * tt;
-        group = t[0];
-        start = t[1];
-        count = t[2];
+        if (a.plan[0] != kPlanMagic || a.plan[1] != a.n_items || a.plan[2] != a.n_groups || a.plan[3] != a.plan_tile)
+            return;
+        tok_tiles = a.plan[4] * split;
+    } else {
+        tok_tiles = (a.n_items + TN - 1) / TN;
     }
-    for (int j = tid; j < TN; j += 256) {
+    const int total = tok_tiles * a.row_tiles;
+    if ((int)blockIdx.x >= total) return;
+    const int xcd = blockIdx.x % kXcds;
+    const int id = xcd * (total / kXcds) + min(xcd, total % kXcds) + blockIdx.x / kXcds;
+    const int t0 = id / (kTokGroup * a.row_tiles) * kTokGroup;
+    const int tw = min(kTokGroup, tok_tiles - t0);
+    const int in = id - t0 * a.row_tiles;
+    const int rt = in / tw, tt = t0 + in % tw;
+
+    const int out_rows = a.swiglu ? S::kTM / 2 : S::kTM;
+    const int row0 = rt * out_rows;
+    int group = 0, start = tt * TN, count = min(TN, a.n_items - start);
+    if (a.plan) {
+        const int* t = a.plan + a.tiles_at + 4 * (tt / split);
+        const int skip = tt % split * TN;
+        group = t[0];
+        start = t[1] + skip;
+        count = min(TN, t[2] - skip);
+        if (count <= 0) return;
+    }
+    for (int j = tid; j < TN; j += S::kNT) {
         const int at = start + min(j, count - 1);
         s_item[j] = a.plan ? a.plan[a.order_at + at] : at;
     }
     __syncthreads();
     if (a.plan && group >= a.n_groups) {   // ids that are no group
-        for (int i = tid; i < count * out_rows; i += 256) {
+        for (int i = tid; i < count * out_rows; i += S::kNT) {
             const int r = row0 + i % out_rows;
             if (r < a.rows)
                 store_y(a.y, a.y_type, (int64_t)s_item[i / out_rows] * a.ldy + r, __builtin_nanf(""));
@@ -374,37 +422,33 @@ __global__ __launch_bounds__(256) void tile_kernel(const TileDev a) {
     else
         wrow = min(row0 + ur, a.rows - 1);
     const uint8_t* W = a.W + group * a.estride;
-    // and its activations: eight columns of TN / 32 tokens
-    constexpr int kXL = TN / 32;
+    // and its activations: eight columns of kXL tokens
     const int xc = tid & 7, xt = tid >> 3;
-    const XT* xp[kXL];
+    const XT* xp[S::kXL];
 #pragma unroll
-    for (int i = 0; i < kXL; ++i) {
-        const int p = s_item[xt + 32 * i];
+    for (int i = 0; i < S::kXL; ++i) {
+        const int p = s_item[xt + S::kNT / 8 * i];
         xp[i] = static_cast<const XT*>(a.x) + (int64_t)(p / a.top_k) * a.xs_tok + (int64_t)(p % a.top_k) * a.xs_slot +
                 8 * xc;
     }
     const bool vec = a.vec != 0;
-    typename U::Raw raw;
-    X8<XT> xr[kXL];
-
-    auto load = [&](int s) __attribute__((always_inline)) {
-        U::fetch(W, wrow, a.nb, min(kTileBlks * s + ub, a.nb - 1), raw);
-        const bool in = kTileBlks * s + (xc >> 2) < a.nb;
-#pragma unroll
-        for (int i = 0; i < kXL; ++i) {
-            if (in)
-                xr[i].load(xp[i] + 64 * s, vec);
-            else
-                xr[i].zero();
-        }
+    struct Stage {
+        typename U::Raw w;
+        X8<XT> x[S::kXL];
     };
-    auto store = [&](int s) __attribute__((always_inline)) {
+    // Whole steps; a row of an odd number of blocks has half a step more.
+    const int steps = a.nb / kTileBlks;
+    auto load = [&](int s, Stage& g) __attribute__((always_inline)) {
+        s = min(s, steps - 1);        // past the last: the last again, unused
+        U::fetch(W, wrow, a.nb, kTileBlks * s + ub, g.w);
+#pragma unroll
+        for (int i = 0; i < S::kXL; ++i) g.x[i].load(xp[i] + 64 * s, vec);
+    };
+    auto put = [&](int s, int blk, bool live, const Stage& g) __attribute__((always_inline)) {
         uint8_t* buf = lds + (s & 1) * S::kBuf;
-        const int blk = kTileBlks * s + ub;
         uint32_t q[8];
         float sc[U::kSub], mu = 0.f;
-        U::decode(raw, min(blk, a.nb - 1), q, sc, mu);
+        U::decode(g.w, blk, q, sc, mu);
         u32x4* w = reinterpret_cast<u32x4*>(buf + ur * kTilePitch + 64 * ub);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
@@ -413,23 +457,23 @@ __global__ __launch_bounds__(256) void tile_kernel(const TileDev a) {
                          XOp<XT>::pair(sbyte(q[2 * i + 1], 0), sbyte(q[2 * i + 1], 1)),
                          XOp<XT>::pair(sbyte(q[2 * i + 1], 2), sbyte(q[2 * i + 1], 3))};
         float* sp = reinterpret_cast<float*>(buf + S::kW + S::kX);
-        const bool in = blk < a.nb;       // past the row: activations and scales are 0
 #pragma unroll
-        for (int h = 0; h < U::kSub; ++h) sp[(ub * U::kSub + h) * kTileRows + ur] = in ? sc[h] : 0.f;
-        float* mp = reinterpret_cast<float*>(buf + S::kW + S::kX + S::kS);
-        if constexpr (U::kSums) mp[ub * kTileRows + ur] = in ? mu : 0.f;
+        for (int h = 0; h < U::kSub; ++h) sp[(ub * U::kSub + h) * S::kTM + ur] = live ? sc[h] : 0.f;
+        u32x4* mp = reinterpret_cast<u32x4*>(buf + S::kW + S::kX + S::kS);     // [block][rows], [block][tokens]
+        if constexpr (U::kSums) mp[ub * S::kTM + ur] = min_operand<0>(live ? mu : 0.f);
 #pragma unroll
-        for (int i = 0; i < kXL; ++i) {
+        for (int i = 0; i < S::kXL; ++i) {
+            const int tok = xt + S::kNT / 8 * i;
             u32x4 p[S::kP];
-            xr[i].pieces(p);
+            g.x[i].pieces(p);
 #pragma unroll
             for (int k = 0; k < S::kP; ++k)
-                *reinterpret_cast<u32x4*>(buf + S::kW + (k * TN + xt + 32 * i) * kTilePitch + 16 * xc) = p[k];
+                *reinterpret_cast<u32x4*>(buf + S::kW + (k * TN + tok) * kTilePitch + 16 * xc) = p[k];
             if constexpr (U::kSums) {
-                float t = xr[i].sum();      // of 8 columns; four lanes hold a block's 32
+                float t = g.x[i].sum();      // of 8 columns; four lanes hold a block's 32
                 t += dpp_mov<0xB1>(t);
                 t += dpp_mov<0x4E>(t);
-                if ((xc & 3) == 0) mp[kTileBlks * kTileRows + (xc >> 2) * TN + xt + 32 * i] = t;
+                if ((xc & 3) == 0) mp[kTileBlks * S::kTM + (xc >> 2) * TN + tok] = min_operand<1>(t);
             }
         }
     };
@@ -443,76 +487,137 @@ __global__ __launch_bounds__(256) void tile_kernel(const TileDev a) {
         for (int t = 0; t < S::kTS; ++t)
 #pragma unroll
             for (int i = 0; i < 16; ++i) acc[r][t][i] = 0.f;
-    f32x16 zero;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) zero[i] = 0.f;
 
+    // The MFMAs of one 32 x 32 piece of a block go between the scalings of
+    // the piece before it: a piece's results are 16 fused multiply-adds a
+    // lane, about as long as its two MFMAs, and the two pipes then run side
+    // by side with no more than two pieces' results live.  Operands are read
+    // from LDS one piece (weights) or one block (activations) ahead.
     auto compute = [&](int s) __attribute__((always_inline)) {
         const uint8_t* buf = lds + (s & 1) * S::kBuf;
-        const float* sp = reinterpret_cast<const float*>(buf + S::kW + S::kX);
-        const float* mp = reinterpret_cast<const float*>(buf + S::kW + S::kX + S::kS);
+        const float* sp = reinterpret_cast<const float*>(buf + S::kW + S::kX) + wr + lr;
+        const uint8_t* wp = buf + (wr + lr) * kTilePitch + 16 * lh;
+        const uint8_t* xq0 = buf + S::kW + (wt + lr) * kTilePitch + 16 * lh;
+        constexpr int kPer = S::kRS * S::kTS;          // pieces of a block
+        constexpr int kPieces = kTileBlks * kPer;
+        constexpr int kMf = 2 * S::kP;                 // MFMAs of a piece
+        f32x16 dot[2][U::kSub];
+        float d[2][U::kSub];
+        u32x4 wq[2][2], xq[2][S::kP][S::kTS][2];
+        auto read_w = [&](auto nc) __attribute__((always_inline)) {     // block and rows number nc
+            constexpr int n = decltype(nc)::value, b = n / S::kRS, r = n % S::kRS;
 #pragma unroll
-        for (int b = 0; b < kTileBlks; ++b) {
-            u32x4 wq[S::kRS][2], xq[S::kP][S::kTS][2];
+            for (int h = 0; h < 2; ++h)
+                wq[n & 1][h] = *reinterpret_cast<const u32x4*>(wp + 32 * r * kTilePitch + 64 * b + 32 * h);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
+            for (int h = 0; h < U::kSub; ++h) d[n & 1][h] = sp[(b * U::kSub + h) * S::kTM + 32 * r];
+        };
+        auto read_x = [&](auto bc) __attribute__((always_inline)) {
+            constexpr int b = decltype(bc)::value;
 #pragma unroll
-                for (int r = 0; r < S::kRS; ++r)
-                    wq[r][h] = *reinterpret_cast<const u32x4*>(buf + (wr + 32 * r + lr) * kTilePitch + 64 * b + 32 * h +
-                                                               16 * lh);
+            for (int k = 0; k < S::kP; ++k)
 #pragma unroll
-                for (int k = 0; k < S::kP; ++k)
+                for (int u = 0; u < S::kTS; ++u)
 #pragma unroll
-                    for (int t = 0; t < S::kTS; ++t)
-                        xq[k][t][h] = *reinterpret_cast<const u32x4*>(
-                            buf + S::kW + (k * TN + wt + 32 * t + lr) * kTilePitch + 64 * b + 32 * h + 16 * lh);
+                    for (int h = 0; h < 2; ++h)
+                        xq[b & 1][k][u][h] =
+                            *reinterpret_cast<const u32x4*>(xq0 + (k * TN + 32 * u) * kTilePitch + 64 * b + 32 * h);
+        };
+        read_x(std::integral_constant<int, 0>{});
+        read_w(std::integral_constant<int, 0>{});
+        float dp[U::kSub];                             // scales of the piece before
+        static_for(std::make_integer_sequence<int, kPieces + 1>{}, [&](auto nc) __attribute__((always_inline)) {
+            constexpr int n = decltype(nc)::value;
+            constexpr int b = n / kPer, r = n / S::kTS % S::kRS, t = n % S::kTS, wn = n / S::kTS;
+            constexpr int pn = n > 0 ? n - 1 : 0, pr = pn / S::kTS % S::kRS, pt = pn % S::kTS;
+            if constexpr (n > 0) {
+#pragma unroll
+                for (int h = 0; h < U::kSub; ++h) dp[h] = d[(pn / S::kTS) & 1][h];
             }
+            static_for(std::make_integer_sequence<int, kMf>{}, [&](auto mc) __attribute__((always_inline)) {
+                constexpr int m = decltype(mc)::value;
+                constexpr int h = m / S::kP, k = m % S::kP;
+                if constexpr (n < kPieces) {
+                    constexpr int o = U::kSub == 2 ? h : 0;
+                    f32x16 c;
+                    if constexpr (k == 0 && (U::kSub == 2 || h == 0)) {
 #pragma unroll
-            for (int r = 0; r < S::kRS; ++r) {
-                float d[U::kSub], mu = 0.f;
-#pragma unroll
-                for (int h = 0; h < U::kSub; ++h) d[h] = sp[(b * U::kSub + h) * kTileRows + wr + 32 * r + lr];
-                if constexpr (U::kSums) mu = mp[b * kTileRows + wr + 32 * r + lr];
-#pragma unroll
-                for (int t = 0; t < S::kTS; ++t) {
-                    f32x16 dot[U::kSub];
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const int o = U::kSub == 2 ? h : 0;
-#pragma unroll
-                        for (int k = 0; k < S::kP; ++k)
-                            dot[o] = XOp<XT>::mfma(xq[k][t][h], wq[r][h], (k == 0 && (U::kSub == 2 || h == 0)) ? zero : dot[o]);
+                        for (int i = 0; i < 16; ++i) c[i] = 0.f;
+                    } else {
+                        c = dot[n & 1][o];
                     }
-#pragma unroll
-                    for (int o = 0; o < U::kSub; ++o)
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) acc[r][t][i] = __builtin_fmaf(d[o], dot[o][i], acc[r][t][i]);
-                    if constexpr (U::kSums) {
-                        const float* sx = mp + kTileBlks * kTileRows + b * TN + wt + 32 * t + 4 * lh;
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const f32x4 v = *reinterpret_cast<const f32x4*>(sx + 8 * i);
-#pragma unroll
-                            for (int j = 0; j < 4; ++j)
-                                acc[r][t][4 * i + j] = __builtin_fmaf(mu, v[j], acc[r][t][4 * i + j]);
-                        }
-                    }
+                    dot[n & 1][o] = XOp<XT>::mfma(xq[b & 1][k][t][h], wq[wn & 1][h], c);
                 }
-            }
+                if constexpr (n > 0) {
+                    // the m-th share of the piece before
+                    constexpr int all = 16 * U::kSub, i0 = all * m / kMf, i1 = all * (m + 1) / kMf;
+#pragma unroll
+                    for (int i = i0; i < i1; ++i)
+                        acc[pr][pt][i & 15] = __builtin_fmaf(dp[i >> 4], dot[pn & 1][i >> 4][i & 15], acc[pr][pt][i & 15]);
+                }
+                // operands of the next rows and block, once the last piece
+                // that reads their registers is past
+                if constexpr (m == 0 && n < kPieces && t == 0 && wn + 1 < kTileBlks * S::kRS)
+                    read_w(std::integral_constant<int, wn + 1>{});
+                if constexpr (m == kMf - 1 && n < kPieces && r == 0 && t == 0 && b + 1 < kTileBlks)
+                    read_x(std::integral_constant<int, b + 1>{});
+                __builtin_amdgcn_sched_barrier(0x4 | 0x10);            // scalar and global memory may pass
+            });
+            // the scalings stay here (they are used a step later only)
+            if constexpr (n > 0) asm volatile("" : "+v"(acc[pr][pt]));
+        });
+        if constexpr (U::kSums) {
+            // mu times the block sums of x, both blocks of the step in one MFMA
+            const u32x4* mp = reinterpret_cast<const u32x4*>(buf + S::kW + S::kX + S::kS);
+            u32x4 mw[S::kRS], mx[S::kTS];
+#pragma unroll
+            for (int r = 0; r < S::kRS; ++r) mw[r] = mp[lh * S::kTM + wr + 32 * r + lr];
+#pragma unroll
+            for (int t = 0; t < S::kTS; ++t) mx[t] = mp[kTileBlks * S::kTM + lh * TN + wt + 32 * t + lr];
+#pragma unroll
+            for (int r = 0; r < S::kRS; ++r)
+#pragma unroll
+                for (int t = 0; t < S::kTS; ++t) acc[r][t] = XOp<__bf16>::mfma(mx[t], mw[r], acc[r][t]);
         }
     };
 
     // One barrier a step: the buffer of step s + 1 was last read in step
-    // s - 1, before the barrier that ended it.
-    const int steps = (a.nb + kTileBlks - 1) / kTileBlks;
-    load(0);
-    store(0);
-    if (steps > 1) load(1);
-    __syncthreads();
-    for (int s = 0; s < steps; ++s) {
-        compute(s);
-        if (s + 1 < steps) store(s + 1);
-        if (s + 2 < steps) load(s + 2);
+    // s - 1, before the barrier that ended it.  A step's loads are issued two
+    // steps before they are put in LDS.
+    if (steps > 0) {
+        Stage g0, g1;
+        load(0, g0);
+        load(1, g1);
+        put(0, ub, true, g0);
+        load(2, g0);
+        __syncthreads();
+        for (int s = 0; s < steps; s += 2) {
+            compute(s);
+            put(s + 1, kTileBlks * (s + 1) + ub, true, g1);      // past the last step: not read
+            load(s + 3, g1);
+            __syncthreads();
+            if (s + 1 >= steps) break;
+            compute(s + 1);
+            put(s + 2, kTileBlks * (s + 2) + ub, true, g0);
+            load(s + 4, g0);
+            __syncthreads();
+        }
+    }
+    if (a.nb % kTileBlks) {
+        // the last block; activations and scales past the row are 0
+        Stage g;
+        U::fetch(W, wrow, a.nb, a.nb - 1, g.w);
+#pragma unroll
+        for (int i = 0; i < S::kXL; ++i) {
+            if (xc < 4)
+                g.x[i].load(xp[i] + 64 * steps, vec);
+            else
+                g.x[i].zero();
+        }
+        __syncthreads();
+        put(steps, a.nb - 1, ub == 0, g);
+        __syncthreads();
+        compute(steps);
         __syncthreads();
     }
 
@@ -526,7 +631,7 @@ __global__ __launch_bounds__(256) void tile_kernel(const TileDev a) {
             for (int i = 0; i < 16; ++i)
                 out[(wt + 32 * t + 8 * (i >> 2) + 4 * lh + (i & 3)) * S::kOutPitch + wr + 32 * r + lr] = acc[r][t][i];
     __syncthreads();
-    for (int i = tid; i < count * out_rows; i += 256) {
+    for (int i = tid; i < count * out_rows; i += S::kNT) {
         const int j = i / out_rows, r = i % out_rows;
         if (row0 + r >= a.rows) continue;
         float v = out[j * S::kOutPitch + r];
@@ -536,9 +641,9 @@ __global__ __launch_bounds__(256) void tile_kernel(const TileDev a) {
 }
 
 template <class F, class XT, int TN>
-int32_t launch_tile(const TileCall& c, hipStream_t st) {
+int32_t launch_tile(const TileCall& c, int plan_tile, hipStream_t st) {
     using S = TileShape<F, XT, TN>;
-    const int out_rows = c.swiglu ? kTileRows / 2 : kTileRows;
+    const int out_rows = c.swiglu ? S::kTM / 2 : S::kTM;
     TileDev d;
     d.W = c.W;
     d.estride = c.estride;
@@ -549,6 +654,7 @@ int32_t launch_tile(const TileCall& c, hipStream_t st) {
     d.n_items = (int)c.n_items;
     d.n_groups = c.n_groups;
     d.top_k = c.top_k;
+    d.plan_tile = plan_tile;
     d.x = c.x;
     d.xs_tok = c.xs_tok;
     d.xs_slot = c.xs_slot;
@@ -560,21 +666,28 @@ int32_t launch_tile(const TileCall& c, hipStream_t st) {
     d.vec = aligned(c.x, 16) && c.xs_tok % per16 == 0 && c.xs_slot % per16 == 0;
     d.tiles_at = (int)plan_tiles_at(c.n_groups);
     d.order_at = c.plan ? (int)plan_order_at(c.n_items, c.n_groups) : 0;
-    const int64_t tiles = c.plan ? plan_tile_bound(c.n_items, c.n_groups, TN) : (c.n_items + TN - 1) / TN;
+    const int64_t tiles = c.plan ? plan_tile_bound(c.n_items, c.n_groups, plan_tile) * (plan_tile / TN)
+                                 : (c.n_items + TN - 1) / TN;
     if (tiles * d.row_tiles > 0x7fffffff)
         return fail(QMV_EINVAL, "qmv: %lld tiles exceed a launch", (long long)(tiles * d.row_tiles));
     auto kern = tile_kernel<F, XT, TN>;
     size_t dyn_max = 0;
     if (const int32_t e = lds_limit(reinterpret_cast<const void*>(kern), kLdsMax, "qmv", &dyn_max)) return e;
     if ((size_t)S::kLds > dyn_max) return fail(QMV_EHIP, "qmv: the tile kernel's LDS exceeds the device's");
-    hipLaunchKernelGGL(kern, dim3((unsigned)(tiles * d.row_tiles)), dim3(256), S::kLds, st, d);
+    hipLaunchKernelGGL(kern, dim3((unsigned)(tiles * d.row_tiles)), dim3(S::kNT), S::kLds, st, d);
     return check_launch("qmv");
 }
 
+// fp32 activations take three times the LDS and MFMAs: 64 tokens by 256 rows
+// where 16-bit ones take 128 by 128.
 template <class F, class XT>
 int32_t launch_tile_n(const TileCall& c, hipStream_t st) {
     const int tile = c.plan ? plan_tile(c.n_items, c.n_groups) : plan_tile(c.n_items, 1);
-    return tile == 32 ? launch_tile<F, XT, 32>(c, st) : launch_tile<F, XT, 128>(c, st);
+    if (tile == 32) return launch_tile<F, XT, 32>(c, 32, st);
+    if constexpr (std::is_same<XT, float>::value)
+        return launch_tile<F, XT, 64>(c, tile, st);
+    else
+        return launch_tile<F, XT, 128>(c, tile, st);
 }
 
 template <class F>
