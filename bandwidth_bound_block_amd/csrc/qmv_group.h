@@ -30,6 +30,16 @@ inline int64_t plan_order_at(int64_t n_items, int n_groups) {
     return plan_tiles_at(n_groups) + 4 * plan_tile_bound(n_items, n_groups, plan_tile(n_items, n_groups));
 }
 
+// Low-rank adapters added to a product without a plan (rank 0: none): item t
+// gains sum_r B[ids[t]][row][r] v[t][r], v summed over its parts.
+struct LoraTile {
+    const void* B;          // [n_adapters][rows][rank] of b_type
+    const int32_t* ids;
+    const float* v;         // [parts][n_items][rank]
+    int32_t b_type, n_adapters, rank, parts;
+    int32_t vec;            // rows of B may be read in 16-byte pieces
+};
+
 // One tiled product.  plan == nullptr: one matrix, the items are rows
 // 0..n_items-1 of x (top_k = 1) and of y.
 struct TileCall {
@@ -48,6 +58,7 @@ struct TileCall {
     int32_t y_type;
     int64_t ldy;          // elements from one item's outputs to the next
     bool swiglu;
+    LoraTile lora;
 };
 // Launches it (arguments already checked); one per format.
 int32_t tile_q8_0(const TileCall& c, hipStream_t st);

@@ -217,7 +217,7 @@ int32_t grouped_entry(const char* name, bool swiglu, qmv_fmt fmt, const void* W,
     if (!aligned(plan, 16)) return fail(QMV_EALIGN, "%s: plan must be 16-byte aligned", name);
     if (!aligned(x, x_elem(x_type)) || !aligned(y, x_elem(y_type)))
         return fail(QMV_EALIGN, "%s: x and the output must be aligned to their element size", name);
-    TileCall c;
+    TileCall c{};
     c.W = static_cast<const uint8_t*>(W);
     c.estride = E > 1 ? estride : 0;
     c.rows = rows;
