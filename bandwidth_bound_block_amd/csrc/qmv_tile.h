@@ -69,52 +69,59 @@ template <> struct XOp<_Float16> {
 };
 
 // --------------------------------------------------------------- weights
-// Experts may follow each other at 2-byte strides (34- and 18-byte blocks),
-// while the blocks' fetches go by the block's parity in a matrix that starts
-// on a word: where this one starts 2 bytes past it, the block before the
-// first does.
-template <class F>
-__device__ __forceinline__ void fetch_even(const uint8_t* W, int64_t g, typename F::Raw& r) {
-    const int odd = (int)(reinterpret_cast<uintptr_t>(W) & 2) >> 1;
-    F::fetch(W - odd * F::kBytes, g + odd, r);
-}
-
-// Unit<F>: one 32-weight block of one row.  fetch() issues its loads,
-// decode() leaves the 32 codes in weight order as signed bytes, the scale of
-// each kSub-th of the block, and mu.
+// A wave reads its 32 rows eight blocks at a time: 16-byte pieces of a row
+// with neighbouring lanes on neighbouring pieces, kept in registers while the
+// eight blocks before them are computed, then copied to the wave's part of
+// LDS (its slot).  Loads by block and lane instead (64 lanes on 64 lines) ran
+// at 2.4 TB/s for Q4_0 and 1.5 for Q6_K whatever the number of waves: the
+// cache looks up about one lane's line a cycle.
+//
+// Rows start on 2 bytes (34-, 18- and 210-byte units), pieces on words: the
+// slot's row r holds the bytes from 0 or 2 (sh) bytes before the row's.  The
+// loads go through a buffer that ends with the word that holds the matrix's
+// last byte: words past it read 0, and no word without a byte of the matrix
+// is read.
+//
+// Unit<F> is a format's step of two blocks, 2 J and 2 J + 1 of the eight (J
+// 0..3), of the lane's row: lane half lh leaves the codes of each block b
+// that MFMA h takes from it, elements at(h, lh) .. + 7, as signed bytes
+// q[b][h][0..1], the blocks' scales d[b][.] (one, or one per 16 weights), and
+// mu of block 2 J + lh.
+//   kRow    bytes of eight blocks;  kCpr  pieces of a row;  kPitch  bytes of
+//   a slot's row, an odd number of 16-byte units.
 template <class F> struct Unit;
 
-template <> struct Unit<Q8_0> {
-    static constexpr int kSub = 1;
-    static constexpr bool kSums = false;
-    using Raw = Q8_0::Raw;
-    __device__ static void fetch(const uint8_t* W, int row, int nb, int blk, Raw& r) {
-        fetch_even<Q8_0>(W, (int64_t)row * nb + blk, r);
-    }
-    __device__ static void decode(const Raw& r, int, uint32_t (&q)[8], float (&s)[kSub], float&) {
-        float m;
-        Q8_0::decode(r, s[0], m, q);
-    }
-};
-
-template <> struct Unit<Q4_0> {
-    static constexpr int kSub = 1;
-    static constexpr bool kSums = false;
-    using Raw = Q4_0::Raw;
-    __device__ static void fetch(const uint8_t* W, int row, int nb, int blk, Raw& r) {
-        fetch_even<Q4_0>(W, (int64_t)row * nb + blk, r);
-    }
-    // 16 (c - 8) as signed bytes; d / 16 is exact
-    __device__ static void decode(const Raw& r, int, uint32_t (&q)[8], float (&s)[kSub], float&) {
-        float d, m;
-        uint32_t c[8];
-        Q4_0::decode(r, d, m, c);
+__device__ __forceinline__ uint32_t lds4(const uint8_t* p) { return *reinterpret_cast<const uint32_t*>(p); }
+__device__ __forceinline__ float lds_half(const uint8_t* p) {
+    return half_bits_to_float(*reinterpret_cast<const uint16_t*>(p));
+}
+// N words from p, p 0 or 2 (sh) bytes past a word
+template <int N>
+__device__ __forceinline__ void lds_words(const uint8_t* p, uint32_t sh, uint32_t (&w)[N]) {
+    const uint8_t* a = p - sh;
+    uint32_t v[N + 1];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) signed_nibbles(c[i], q[i], q[4 + i]);
-        s[0] = d * 0.0625f;
-    }
-};
-
+    for (int i = 0; i <= N; ++i) v[i] = lds4(a + 4 * i);
+#pragma unroll
+    for (int i = 0; i < N; ++i) w[i] = __builtin_amdgcn_alignbyte(v[i + 1], v[i], sh);
+}
+// Exchanges the upper 32 lanes of a with the lower 32 of b.
+__device__ __forceinline__ void swap_halves(uint32_t& a, uint32_t& b) {
+    const auto r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
+    a = r[0];
+    b = r[1];
+}
+// v of lane l % 32 (a) and of lane l % 32 + 32 (b), in both.
+__device__ __forceinline__ void both_halves(uint32_t v, uint32_t& a, uint32_t& b) {
+    a = b = v;
+    swap_halves(a, b);
+}
+__device__ __forceinline__ void both_halves(float v, float& a, float& b) {
+    uint32_t x, y;
+    both_halves(fbits(v), x, y);
+    a = __builtin_bit_cast(float, x);
+    b = __builtin_bit_cast(float, y);
+}
 // c - k per byte, c and k in 0..15: no borrow crosses a byte
 __device__ __forceinline__ uint32_t less_pivot(uint32_t c, uint32_t k4) {
     return ((c | 0x80808080u) - k4) ^ 0x80808080u;
@@ -125,190 +132,131 @@ __device__ __forceinline__ float pivot(float D, float M) {
     return __builtin_fminf(__builtin_fmaxf(__builtin_rintf(M * __builtin_amdgcn_rcpf(D)), 0.f), 15.f);
 }
 
-template <> struct Unit<Q4_1> {
-    static constexpr int kSub = 1;
-    static constexpr bool kSums = true;
-    using Raw = Q4_1::Raw;
-    __device__ static void fetch(const uint8_t* W, int row, int nb, int blk, Raw& r) {
-        Q4_1::fetch(W, (int64_t)row * nb + blk, r);
-    }
-    __device__ static void decode(const Raw& r, int, uint32_t (&q)[8], float (&s)[kSub], float& mu) {
-        float d, m;
-        uint32_t c[8];
-        Q4_1::decode(r, d, m, c);
-        const float k = pivot(d, -m);
-        const uint32_t k4 = (uint32_t)k * 0x01010101u;
+template <> struct Unit<Q8_0> {
+    static constexpr int kSub = 1, kRow = 272, kCpr = 18, kPitch = 304;
+    static constexpr bool kSums = false;
+    __device__ static constexpr int at(int h, int lh) { return 16 * lh + 8 * h; }
+    template <int J>
+    __device__ static void step(const uint8_t* row, uint32_t sh, int lh, uint32_t (&q)[2][2][2], float (&d)[2][kSub],
+                                float&) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            q[i] = less_pivot(c[i] & 0x0f0f0f0fu, k4);
-            q[4 + i] = less_pivot((c[i] >> 4) & 0x0f0f0f0fu, k4);
+        for (int b = 0; b < 2; ++b) {
+            const uint8_t* blk = row + sh + 34 * (2 * J + b);     // 2 b (mod 4) past sh
+            uint32_t w[4];
+            lds_words<4>(blk + 2 + 16 * lh, (sh + 2 * b + 2) & 2, w);
+            q[b][0][0] = w[0]; q[b][0][1] = w[1]; q[b][1][0] = w[2]; q[b][1][1] = w[3];
+            d[b][0] = lds_half(blk);
         }
-        s[0] = d;
-        mu = __builtin_fmaf(d, k, m);
     }
 };
 
-// Super-block formats: blk = 8 * super-block + J.
+template <> struct Unit<Q4_0> {
+    static constexpr int kSub = 1, kRow = 144, kCpr = 10, kPitch = 176;
+    static constexpr bool kSums = false;
+    __device__ static constexpr int at(int h, int lh) { return 16 * h + 8 * lh; }
+    // 16 (c - 8) as signed bytes; d / 16 is exact
+    template <int J>
+    __device__ static void step(const uint8_t* row, uint32_t sh, int lh, uint32_t (&q)[2][2][2], float (&d)[2][kSub],
+                                float&) {
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+            const uint8_t* blk = row + sh + 18 * (2 * J + b);     // 2 b (mod 4) past sh
+            uint32_t w[2];
+            lds_words<2>(blk + 2 + 8 * lh, (sh + 2 * b + 2) & 2, w);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) signed_nibbles(w[i], q[b][0][i], q[b][1][i]);
+            d[b][0] = lds_half(blk) * 0.0625f;
+        }
+    }
+};
+
+template <> struct Unit<Q4_1> {
+    static constexpr int kSub = 1, kRow = 160, kCpr = 10, kPitch = 176;
+    static constexpr bool kSums = true;
+    __device__ static constexpr int at(int h, int lh) { return 16 * h + 8 * lh; }
+    template <int J>
+    __device__ static void step(const uint8_t* row, uint32_t, int lh, uint32_t (&q)[2][2][2], float (&d)[2][kSub],
+                                float& mu) {
+        const uint32_t dm = lds4(row + 20 * (2 * J + lh));
+        const float D = half_bits_to_float(dm), m = half_bits_to_float(dm >> 16);
+        const float k = pivot(D, -m);
+        mu = __builtin_fmaf(D, k, m);
+        uint32_t k4[2];
+        both_halves((uint32_t)k * 0x01010101u, k4[0], k4[1]);
+        both_halves(D, d[0][0], d[1][0]);
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const uint32_t c = lds4(row + 20 * (2 * J + b) + 4 + 8 * lh + 4 * i);
+                q[b][0][i] = less_pivot(c & 0x0f0f0f0fu, k4[b]);
+                q[b][1][i] = less_pivot((c >> 4) & 0x0f0f0f0fu, k4[b]);
+            }
+    }
+};
+
+// Super-block formats: the eight blocks are a super-block.
 struct Q4KTile {};
 template <> struct Unit<Q4KTile> {
-    static constexpr int kSub = 1;
+    static constexpr int kSub = 1, kRow = 144, kCpr = 9, kPitch = 144;
     static constexpr bool kSums = true;
-    struct Raw {
-        u32x4 h, a, b;
-    };
-    __device__ static void fetch(const uint8_t* W, int row, int nb, int blk, Raw& r) {
-        const uint8_t* sb = W + ((int64_t)row * (nb >> 3) + (blk >> 3)) * 144;
-        const int o = 16 + 32 * ((blk & 7) >> 1);
-        r.h = *reinterpret_cast<const u32x4*>(sb);
-        r.a = *reinterpret_cast<const u32x4*>(sb + o);
-        r.b = *reinterpret_cast<const u32x4*>(sb + o + 16);
-    }
-    __device__ static void decode(const Raw& r, int blk, uint32_t (&q)[8], float (&s)[kSub], float& mu) {
-        const int J = blk & 7, t = 8 * (J & 3);
-        const uint32_t h1 = r.h.y >> t, h2 = r.h.z >> t, h3 = r.h.w >> t;
-        const uint32_t sc = J < 4 ? (h1 & 63u) : ((h3 & 15u) | ((h1 >> 2) & 48u));
-        const uint32_t mn = J < 4 ? (h2 & 63u) : (((h3 >> 4) & 15u) | ((h2 >> 2) & 48u));
-        const float D = half_bits_to_float(r.h.x) * (float)sc;          // exact
-        const float M = half_bits_to_float(r.h.x >> 16) * (float)mn;    // exact
+    __device__ static constexpr int at(int h, int lh) { return 16 * lh + 8 * h; }
+    template <int J>
+    __device__ static void step(const uint8_t* row, uint32_t, int lh, uint32_t (&q)[2][2][2], float (&d)[2][kSub],
+                                float& mu) {
+        const u32x4 hd = *reinterpret_cast<const u32x4*>(row);
+        const int t = 8 * ((2 * J & 3) + lh);                 // block 2 J + lh: byte J % 4 of the fields
+        const uint32_t h1 = hd.y >> t, h2 = hd.z >> t, h3 = hd.w >> t;
+        const uint32_t sc = J < 2 ? (h1 & 63u) : ((h3 & 15u) | ((h1 >> 2) & 48u));
+        const uint32_t mn = J < 2 ? (h2 & 63u) : (((h3 >> 4) & 15u) | ((h2 >> 2) & 48u));
+        const float D = half_bits_to_float(hd.x) * (float)sc;          // exact
+        const float M = half_bits_to_float(hd.x >> 16) * (float)mn;    // exact
         const float k = pivot(D, M);
-        const uint32_t k4 = (uint32_t)k * 0x01010101u;
-        const uint32_t c[8] = {r.a.x, r.a.y, r.a.z, r.a.w, r.b.x, r.b.y, r.b.z, r.b.w};
-        const int sh = 4 * (J & 1);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) q[i] = less_pivot((c[i] >> sh) & 0x0f0f0f0fu, k4);
-        s[0] = D;
         mu = __builtin_fmaf(D, k, -M);
+        uint32_t k4[2];
+        both_halves((uint32_t)k * 0x01010101u, k4[0], k4[1]);
+        both_halves(D, d[0][0], d[1][0]);
+        const u32x4 c = *reinterpret_cast<const u32x4*>(row + 16 + 32 * J + 16 * lh);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            q[0][i >> 1][i & 1] = less_pivot(c[i] & 0x0f0f0f0fu, k4[0]);
+            q[1][i >> 1][i & 1] = less_pivot((c[i] >> 4) & 0x0f0f0f0fu, k4[1]);
+        }
     }
 };
 
 struct Q6KTile {};
 template <> struct Unit<Q6KTile> {
-    static constexpr int kSub = 2;
+    static constexpr int kSub = 2, kRow = 210, kCpr = 14, kPitch = 240;
     static constexpr bool kSums = false;
-    // The super-block starts sh = 0 or 2 bytes past a word; words from
-    // sb - sh (inside the matrix: sh = 2 only past its first super-block).
-    struct Raw {
-        u32x4 l0, l1, h0, h1;
-        uint32_t l8, h8, sc, d, sh;
-    };
-    __device__ static void fetch(const uint8_t* W, int row, int nb, int blk, Raw& r) {
-        const uint8_t* sb = W + ((int64_t)row * (nb >> 3) + (blk >> 3)) * 210;
-        const int sh = (int)(reinterpret_cast<uintptr_t>(sb) & 2);
-        const int J = blk & 7;
-        const uint8_t* pl = sb - sh + 64 * (J >> 2) + 32 * (J & 1);
-        const uint8_t* ph = sb - sh + 128 + 32 * (J >> 2);
-        r.l0 = ld16(pl);
-        r.l1 = ld16(pl + 16);
-        r.l8 = ld4(pl + 32);
-        r.h0 = ld16(ph);
-        r.h1 = ld16(ph + 16);
-        r.h8 = ld4(ph + 32);
-        r.sc = ld2(sb + 192 + 2 * J);
-        r.d = ld2(sb + 208);
-        r.sh = (uint32_t)sh;
-    }
+    __device__ static constexpr int at(int h, int lh) { return 16 * h + 8 * lh; }     // an MFMA is one scale's 16 weights
     // 4 (c - 32) as signed bytes; d sc / 4 is exact
-    __device__ static void decode(const Raw& r, int blk, uint32_t (&q)[8], float (&s)[kSub], float&) {
-        const int qt = blk & 3;
-        const uint32_t l[9] = {r.l0.x, r.l0.y, r.l0.z, r.l0.w, r.l1.x, r.l1.y, r.l1.z, r.l1.w, r.l8};
-        const uint32_t h[9] = {r.h0.x, r.h0.y, r.h0.z, r.h0.w, r.h1.x, r.h1.y, r.h1.z, r.h1.w, r.h8};
-        const int sl = qt < 2 ? 0 : 4, su = 6 - 2 * qt;
+    template <int J>
+    __device__ static void step(const uint8_t* row, uint32_t sh, int lh, uint32_t (&q)[2][2][2], float (&d)[2][kSub],
+                                float&) {
+        const uint8_t* sb = row + sh;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const uint32_t lo = __builtin_amdgcn_alignbyte(l[i + 1], l[i], r.sh) >> sl;
-            const uint32_t hi = (__builtin_amdgcn_alignbyte(h[i + 1], h[i], r.sh) ^ 0xaaaaaaaau) << su;
-            q[i] = ((lo << 2) & 0x3c3c3c3cu) | (hi & 0xc0c0c0c0u);
+        for (int h = 0; h < 2; ++h) {
+            uint32_t hi[2];
+            lds_words<2>(sb + 128 + 32 * (J >> 1) + 16 * h + 8 * lh, sh, hi);
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                uint32_t lo[2];
+                lds_words<2>(sb + 64 * (J >> 1) + 32 * b + 16 * h + 8 * lh, sh, lo);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const uint32_t l = J & 1 ? lo[i] >> 2 : lo[i] << 2;
+                    q[b][h][i] = (l & 0x3c3c3c3cu) | (((hi[i] ^ 0xaaaaaaaau) << (6 - 2 * (2 * (J & 1) + b))) & 0xc0c0c0c0u);
+                }
+            }
         }
-        const float d4 = half_bits_to_float(r.d) * 0.25f;
-        s[0] = d4 * (float)(int8_t)(r.sc & 0xff);
-        s[1] = d4 * (float)(int8_t)(r.sc >> 8);
-    }
-};
-
-// --------------------------------------------------------------- slots
-// Eight blocks of each of a wave's 32 rows, loaded as 16-byte pieces with
-// neighbouring lanes on neighbouring pieces, kept in registers while the
-// blocks before them are computed, then copied to the wave's part of LDS
-// (its slot), where each lane takes its block.  Loads by block and lane
-// instead (64 lanes on 64 lines) run at 2.4 TB/s for Q4_0 and 1.5 for Q6_K
-// whatever the number of waves: the cache looks up one lane's line a cycle.
-// kCpr: pieces of a row; kPitch: bytes of a row in the slot, an odd number of
-// 16-byte units.  take() leaves what Unit<F>::fetch would.
-template <class F, int BYTES, int PITCH>
-struct SlotOf {
-    static constexpr int kRow = BYTES, kCpr = BYTES / 16, kPitch = PITCH;
-    static constexpr int kLoads = (32 * kCpr + 63) / 64;
-    struct Regs {
-        u32x4 v[kLoads];
-    };
-    // the lane's piece k: row and byte of the row
-    __device__ static int row_of(int k, int lane) { return min(64 * k + lane, 32 * kCpr - 1) / kCpr; }
-    __device__ static int byte_of(int k, int lane) { return min(64 * k + lane, 32 * kCpr - 1) % kCpr * 16; }
-    __device__ static void load(const uint8_t* W, const uint32_t (&off)[kLoads], uint32_t, int sup, Regs& r) {
-        const uint8_t* p = W + (int64_t)sup * kRow;
+        uint32_t sc[1];
+        lds_words<1>(sb + 192 + 4 * J, sh, sc);
+        const float d4 = lds_half(sb + 208) * 0.25f;
 #pragma unroll
-        for (int k = 0; k < kLoads; ++k) r.v[k] = *reinterpret_cast<const u32x4*>(p + off[k]);
-    }
-    __device__ static void put(const Regs& r, uint8_t* slot, const uint8_t*, uint32_t, int, int lane) {
+        for (int b = 0; b < 2; ++b)
 #pragma unroll
-        for (int k = 0; k < kLoads; ++k)
-            *reinterpret_cast<u32x4*>(slot + row_of(k, lane) * kPitch + byte_of(k, lane)) = r.v[k];
-    }
-};
-template <class F> struct Slot;
-template <> struct Slot<Q8_0> : SlotOf<Q8_0, 272, 272> {
-    __device__ static void take(const uint8_t* row, const uint8_t*, int l, Q8_0::Raw& r) { Q8_0::from_lds(row, l, r); }
-};
-template <> struct Slot<Q4_0> : SlotOf<Q4_0, 144, 144> {
-    __device__ static void take(const uint8_t* row, const uint8_t*, int l, Q4_0::Raw& r) { Q4_0::from_lds(row, l, r); }
-};
-template <> struct Slot<Q4_1> : SlotOf<Q4_1, 160, 176> {
-    __device__ static void take(const uint8_t* row, const uint8_t*, int l, Q4_1::Raw& r) { Q4_1::from_lds(row, l, r); }
-};
-template <> struct Slot<Q4KTile> : SlotOf<Q4KTile, 144, 144> {
-    __device__ static void take(const uint8_t* row, const uint8_t*, int l, Unit<Q4KTile>::Raw& r) {
-        const u32x4* q = reinterpret_cast<const u32x4*>(row + 16 + 32 * (l >> 1));
-        r.h = *reinterpret_cast<const u32x4*>(row);
-        r.a = q[0];
-        r.b = q[1];
-    }
-};
-// Q6_K: 13 pieces from the word the super-block starts in (0 or 2 bytes
-// before it), and its last four bytes on their own: every load stays inside.
-template <> struct Slot<Q6KTile> : SlotOf<Q6KTile, 210, 240> {
-    struct Regs {
-        u32x4 v[kLoads];
-        uint32_t t0, t1;
-    };
-    __device__ static void load(const uint8_t* W, const uint32_t (&off)[kLoads], uint32_t own, int sup, Regs& r) {
-        const uint8_t* p = W + (int64_t)sup * kRow;
-#pragma unroll
-        for (int k = 0; k < kLoads; ++k)     // off: of the piece; whole words before it do not change the parity
-            r.v[k] = ld16(reinterpret_cast<const uint8_t*>(reinterpret_cast<uintptr_t>(p + off[k]) & ~(uintptr_t)3));
-        r.t0 = ld2(p + own + 206);
-        r.t1 = ld2(p + own + 208);
-    }
-    __device__ static void put(const Regs& r, uint8_t* slot, const uint8_t* W, uint32_t own, int sup, int lane) {
-#pragma unroll
-        for (int k = 0; k < kLoads; ++k)
-            *reinterpret_cast<u32x4*>(slot + row_of(k, lane) * kPitch + byte_of(k, lane)) = r.v[k];
-        const bool odd = (reinterpret_cast<uintptr_t>(W + (int64_t)sup * kRow + own) & 2) != 0;
-        *reinterpret_cast<uint32_t*>(slot + (lane & 31) * kPitch + 208) = odd ? (r.t0 | (r.t1 << 16)) : r.t1;
-    }
-    // at: the super-block's address
-    __device__ static void take(const uint8_t* row, const uint8_t* at, int l, Unit<Q6KTile>::Raw& r) {
-        const int sh = (int)(reinterpret_cast<uintptr_t>(at) & 2);
-        const uint8_t* pl = row + 64 * (l >> 2) + 32 * (l & 1);
-        const uint8_t* ph = row + 128 + 32 * (l >> 2);
-        r.l0 = *reinterpret_cast<const u32x4*>(pl);
-        r.l1 = *reinterpret_cast<const u32x4*>(pl + 16);
-        r.l8 = ld4(pl + 32);
-        r.h0 = *reinterpret_cast<const u32x4*>(ph);
-        r.h1 = *reinterpret_cast<const u32x4*>(ph + 16);
-        r.h8 = ld4(ph + 32);
-        r.sc = ld2(row + sh + 192 + 2 * l);
-        r.d = ld2(row + sh + 208);
-        r.sh = (uint32_t)sh;
+            for (int h = 0; h < 2; ++h) d[b][h] = d4 * (float)(int8_t)(sc[0] >> (8 * (2 * b + h)));
     }
 };
 
@@ -416,20 +364,6 @@ __device__ __forceinline__ void store_y(void* y, int y_type, int64_t at, float v
     } else {
         static_cast<__bf16*>(y)[at] = (__bf16)v;
     }
-}
-
-// Exchanges the upper 32 lanes of a with the lower 32 of b.
-__device__ __forceinline__ void swap_halves(uint32_t& a, uint32_t& b) {
-    const auto r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
-    a = r[0];
-    b = r[1];
-}
-// v of lane l % 32 (a) and of lane l % 32 + 32 (b), in both.
-__device__ __forceinline__ void both_halves(float v, float& a, float& b) {
-    uint32_t x = fbits(v), y = fbits(v);
-    swap_halves(x, y);
-    a = __builtin_bit_cast(float, x);
-    b = __builtin_bit_cast(float, y);
 }
 
 constexpr int kTileWaves = 4;
@@ -555,15 +489,13 @@ __device__ __forceinline__ void add_adapters(const LoraTile& l, const int* s_ada
 constexpr int kXcds = 8;          // workgroups go to the XCDs in turn
 constexpr int kTokGroup = 8;      // token tiles that an XCD takes together
 // A wave takes 32 weight rows by TN tokens.  Its step is two blocks of each
-// row: lane l holds block l / 32 of row l % 32, decodes it alone, and one
-// exchange of lane halves turns the two blocks' codes into MFMA operands, so
-// no wave waits for another's weights.  KG waves of a workgroup share 32 rows
-// and take their eight-block pieces of the row (four steps) in turn; their
-// sums are added in a fixed order at the end: where there are few rows, that
-// keeps enough loads in flight.  Activations are staged in LDS in chunks of
-// CHS steps for each of the KG.  SLOT: weights by whole lines through LDS;
-// otherwise (rows off 16 bytes, or of part of eight blocks) by each lane.
-template <class F, class XT, int TN, int KG, bool SLOT>
+// row, decoded by the lanes that multiply them, so no wave waits for
+// another's weights.  KG waves of a workgroup share 32 rows and take their
+// eight-block pieces of the row (four steps) in turn; their sums are added in
+// a fixed order at the end: where there are few rows, that keeps enough loads
+// in flight.  Activations are staged in LDS in chunks of CHS steps for each
+// of the KG.
+template <class F, class XT, int TN, int KG>
 struct TileShape {
     static constexpr int kP = XOp<XT>::kPieces;
     static constexpr int kTM = 32 * kTileWaves / KG;
@@ -571,14 +503,14 @@ struct TileShape {
     static constexpr int kCHS = TN > 32 || kP > 1 || KG > 1 ? 1 : 2;
     // waves of a SIMD that the registers are cut for; few tokens leave the
     // decoding as the bound, and it takes four waves to keep that going
-    static constexpr int kOcc = TN > 32 ? 2 : (kP > 1 ? 3 : 4);
+    static constexpr int kOcc = TN > 32 || kP > 1 ? 2 : 3;
     static constexpr int kCH = kCHS * KG;
     static constexpr int kXL = TN * 8 * kCH / kTileThreads;         // 8-column pieces of x per thread and chunk
     static constexpr int kPitch = 128 * kCH + 16;                   // bytes of a staged token: an odd number of 16-byte units, so 8 tokens hit distinct banks
     static constexpr int kX = kP * TN * kPitch;
     static constexpr int kM = Unit<F>::kSums ? 2 * kCH * TN * 16 : 0;
     static constexpr int kBuf = kX + kM;
-    static constexpr int kSlot = SLOT ? 32 * Slot<F>::kPitch : 0;   // of a wave
+    static constexpr int kSlot = 32 * Unit<F>::kPitch;              // of a wave
     static constexpr int kOutPitch = kTM + 4;                       // floats
     static constexpr int kOut = KG * TN * kOutPitch * 4;
     static constexpr int kMain = 2 * kBuf + kTileWaves * kSlot;
@@ -588,9 +520,9 @@ struct TileShape {
 };
 
 // LORA: the tokens carry adapters (and there is no plan).
-template <class F, class XT, int TN, int KG, bool SLOT, bool LORA>
-__global__ __launch_bounds__(kTileThreads, (TileShape<F, XT, TN, KG, SLOT>::kOcc)) void tile_kernel(const TileDev a) {
-    using S = TileShape<F, XT, TN, KG, SLOT>;
+template <class F, class XT, int TN, int KG, bool LORA>
+__global__ __launch_bounds__(kTileThreads, (TileShape<F, XT, TN, KG>::kOcc)) void tile_kernel(const TileDev a) {
+    using S = TileShape<F, XT, TN, KG>;
     using U = Unit<F>;
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
     __shared__ int s_item[TN], s_adapter[LORA ? TN : 1];
@@ -636,38 +568,47 @@ __global__ __launch_bounds__(kTileThreads, (TileShape<F, XT, TN, KG, SLOT>::kOcc
         return a.swiglu ? (r < out_rows ? 0 : a.rows) + min(row0 + (r & (out_rows - 1)), a.rows - 1)
                         : min(row0 + r, a.rows - 1);
     };
-    const int wrow = matrix_row(wr + lr);
-    const uint8_t* W = a.W + min(group, a.n_groups - 1) * a.estride;
-
     // Weights: eight blocks (four steps) of the row at a time.
-    constexpr bool kWhole = SLOT && KG == 1;             // no step passes the row's end
     const int sups = (a.nb + 7) >> 3;                    // pieces of eight blocks of a row
     const int rounds = (sups + KG - 1) / KG;
-    auto sup_of = [&](int s) __attribute__((always_inline)) { return KG * s + wk; };
-    // SLOT: pieces of 16 bytes; otherwise the lane's blocks of steps n, n + 1
-    using SL = Slot<F>;
-    typename SL::Regs wreg;
-    uint32_t woff[SL::kLoads], wown = 0;
-    typename U::Raw r0, r1;
-    auto block_of = [&](int n) __attribute__((always_inline)) { return 8 * sup_of(n >> 2) + 2 * (n & 3) + lh; };
-    auto load_slot = [&](int s) __attribute__((always_inline)) {
-        SL::load(W, woff, wown, min(sup_of(s), sups - 1), wreg);
-    };
-    auto load_lane = [&](int n, typename U::Raw& r) __attribute__((always_inline)) {
-        U::fetch(W, wrow, a.nb, min(block_of(n), a.nb - 1), r);
+    auto sup_of = [&](int s) __attribute__((always_inline)) { return min(KG * s + wk, sups - 1); };
+    const uint32_t pitch = (uint32_t)(a.nb / 8 * U::kRow + a.nb % 8 * (U::kRow / 8));
+    const int first = matrix_row(wr);                    // the wave's rows are at and after it
+    const uint8_t* W = a.W + min(group, a.n_groups - 1) * a.estride;
+    const uintptr_t wbase = reinterpret_cast<uintptr_t>(W + (int64_t)first * pitch);
+    const uintptr_t wend = reinterpret_cast<uintptr_t>(W + (int64_t)(a.swiglu ? 2 * a.rows : a.rows) * pitch);
+    const int64_t wlen = (int64_t)(((wend + 3) & ~(uintptr_t)3) - (wbase & ~(uintptr_t)3));
+    const __amdgpu_buffer_rsrc_t wbuf = raw_buffer(reinterpret_cast<const void*>(wbase & ~(uintptr_t)3),
+                                                   (uint32_t)min(wlen, (int64_t)0xfffffffc));
+    const uint32_t wsh = (uint32_t)(wbase & 2);
+    constexpr int kLoads = (32 * U::kCpr + 63) / 64;
+    // the lane's pieces: row and byte of the row, where in the matrix, where in the slot
+    uint32_t woff[kLoads];
+    int wput[kLoads];
+#pragma unroll
+    for (int k = 0; k < kLoads; ++k) {
+        const int p = min(64 * k + lane, 32 * U::kCpr - 1), r = p / U::kCpr, byte = 16 * (p % U::kCpr);
+        // whole words of 16 past the row's own start: & ~3 leaves the piece's
+        woff[k] = wsh + (uint32_t)(matrix_row(wr + r) - first) * pitch + byte;
+        wput[k] = r * U::kPitch + byte;
+    }
+    const uint32_t wown = wsh + (uint32_t)(matrix_row(wr + lr) - first) * pitch;
+    u32x4 wreg[kLoads];
+    auto load_w = [&](int s) __attribute__((always_inline)) {
+        const int at = sup_of(s) * U::kRow;
+#pragma unroll
+        for (int k = 0; k < kLoads; ++k) {
+            const auto v = __builtin_amdgcn_raw_buffer_load_b128(wbuf, (int)((woff[k] + at) & ~3u), 0, 0);
+            wreg[k] = u32x4{v[0], v[1], v[2], v[3]};
+        }
     };
     uint8_t* slot = lds + 2 * S::kBuf + wave * S::kSlot;
-    if constexpr (SLOT) {
-        const uint32_t pitch = (uint32_t)(sups * SL::kRow);
+    const uint8_t* slot_row = slot + lr * U::kPitch;
+    auto put_w = [&]() __attribute__((always_inline)) {
 #pragma unroll
-        for (int k = 0; k < SL::kLoads; ++k)
-            woff[k] = (uint32_t)matrix_row(wr + SL::row_of(k, lane)) * pitch + (uint32_t)SL::byte_of(k, lane);
-        wown = (uint32_t)wrow * pitch;
-        load_slot(0);
-    } else {
-        load_lane(0, r0);
-        load_lane(1, r1);
-    }
+        for (int k = 0; k < kLoads; ++k) *reinterpret_cast<u32x4*>(slot + wput[k]) = wreg[k];
+    };
+    load_w(0);
 
     if (tid < TN) {
         const int at = start + min(tid, count - 1);
@@ -707,14 +648,18 @@ __global__ __launch_bounds__(kTileThreads, (TileShape<F, XT, TN, KG, SLOT>::kOcc
     auto load_x = [&](int c, XRegs& g) __attribute__((always_inline)) {
         const int at = min(column(c), 32 * a.nb - 8);
 #pragma unroll
-        for (int i = 0; i < S::kXL; ++i) g.x[i].load(xp[i] + at, vec);
+        for (int i = 0; i < S::kXL; ++i)
+            if (xt + kXStep * i < count) g.x[i].load(xp[i] + at, vec);
     };
     auto put_x = [&](int c, XRegs& g) __attribute__((always_inline)) {
         uint8_t* buf = lds + (c & 1) * S::kBuf;
         // only the row's last round can hold columns past it
-        if (!kWhole && 256 * KG * (c / kParts + 1) > 32 * a.nb && column(c) >= 32 * a.nb) {
+        if (256 * KG * (c / kParts + 1) > 32 * a.nb) {
+            asm volatile("");
+            if (column(c) >= 32 * a.nb) {
 #pragma unroll
-            for (int i = 0; i < S::kXL; ++i) g.x[i].zero();
+                for (int i = 0; i < S::kXL; ++i) g.x[i].zero();
+            }
         }
 #pragma unroll
         for (int i = 0; i < S::kXL; ++i) {
@@ -740,33 +685,40 @@ __global__ __launch_bounds__(kTileThreads, (TileShape<F, XT, TN, KG, SLOT>::kOcc
 #pragma unroll
         for (int i = 0; i < 16; ++i) acc[t][i] = 0.f;
 
-    // Step n of the wave, the sc0-th of those staged in buf: decode, then for
+    // Step J of round s, the sc0-th of those staged in buf: decode, then for
     // each block and 32 tokens (a piece) its MFMAs, between the scalings of
     // the piece before it: a piece's results are 16 fused multiply-adds a
     // lane, about as long as its two MFMAs, so the two pipes run side by side
     // with two pieces' results live.
-    auto compute = [&](int n, int sc0, const uint8_t* buf, const typename U::Raw& raw) __attribute__((always_inline)) {
-        const int blk = block_of(n);
-        uint32_t q[8], op[16];
-        float sc[U::kSub], mu = 0.f, d[2][U::kSub];
-        U::decode(raw, blk, q, sc, mu);
+    auto compute = [&](auto jc, int s, int sc0, const uint8_t* buf) __attribute__((always_inline)) {
+        constexpr int J = decltype(jc)::value;
+        const int blk = 8 * (KG * s + wk) + 2 * J;
+        uint32_t q[2][2][2];
+        u32x4 op[2][2];
+        float mu = 0.f, d[2][U::kSub];
+        U::template step<J>(slot_row, (wown + sup_of(s) * U::kRow) & 2, lh, q, d, mu);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            op[2 * j] = XOp<XT>::pair(sbyte(q[j], 0), sbyte(q[j], 1));
-            op[2 * j + 1] = XOp<XT>::pair(sbyte(q[j], 2), sbyte(q[j], 3));
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                op[b][h] = u32x4{XOp<XT>::pair(sbyte(q[b][h][0], 0), sbyte(q[b][h][0], 1)),
+                                 XOp<XT>::pair(sbyte(q[b][h][0], 2), sbyte(q[b][h][0], 3)),
+                                 XOp<XT>::pair(sbyte(q[b][h][1], 0), sbyte(q[b][h][1], 1)),
+                                 XOp<XT>::pair(sbyte(q[b][h][1], 2), sbyte(q[b][h][1], 3))};
+        // past the row the scales are 0 (and so are the activations); the
+        // asm keeps this a branch, which only a row's last round takes
+        if (8 * (KG * s + wk) + 8 > a.nb) {
+            asm volatile("");
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+                if (blk + b >= a.nb) {
+#pragma unroll
+                    for (int h = 0; h < U::kSub; ++h) d[b][h] = 0.f;
+                }
+            if (blk + lh >= a.nb) mu = 0.f;
         }
-        // lanes hold codes 8m..8m+7 of their block in op[4m..4m+3]; after the
-        // exchange op[0..3], op[8..11] are the first block's operands and
-        // op[4..7], op[12..15] the second's
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) swap_halves(op[8 * h + j], op[8 * h + 4 + j]);
-        const bool live = kWhole || blk < a.nb;        // past the row: its scale is 0
-#pragma unroll
-        for (int h = 0; h < U::kSub; ++h) both_halves(live ? sc[h] : 0.f, d[0][h], d[1][h]);
 
-        const uint8_t* xq0 = buf + lr * S::kPitch + 128 * sc0 + 16 * lh;
+        const uint8_t* xq0 = buf + lr * S::kPitch + 128 * sc0 + 2 * U::at(0, 1) * lh;
         constexpr int kPieces = 2 * S::kTS;
         constexpr int kMf = 2 * S::kP;                        // MFMAs of a piece
         f32x16 dot[2][U::kSub];
@@ -778,7 +730,7 @@ __global__ __launch_bounds__(kTileThreads, (TileShape<F, XT, TN, KG, SLOT>::kOcc
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
                     xq[e & 1][k][h] =
-                        *reinterpret_cast<const u32x4*>(xq0 + (k * TN + 32 * t) * S::kPitch + 64 * b + 32 * h);
+                        *reinterpret_cast<const u32x4*>(xq0 + (k * TN + 32 * t) * S::kPitch + 64 * b + 2 * U::at(h, 0));
         };
         read_x(std::integral_constant<int, 0>{});
         static_for(std::make_integer_sequence<int, kPieces + 1>{}, [&](auto nc) __attribute__((always_inline)) {
@@ -791,7 +743,6 @@ __global__ __launch_bounds__(kTileThreads, (TileShape<F, XT, TN, KG, SLOT>::kOcc
                 constexpr int h = m / S::kP, k = m % S::kP;
                 if constexpr (e < kPieces) {
                     constexpr int o = U::kSub == 2 ? h : 0;
-                    constexpr int w = 8 * h + 4 * b;
                     f32x16 c;
                     if constexpr (k == 0 && (U::kSub == 2 || h == 0)) {
 #pragma unroll
@@ -799,7 +750,7 @@ __global__ __launch_bounds__(kTileThreads, (TileShape<F, XT, TN, KG, SLOT>::kOcc
                     } else {
                         c = dot[e & 1][o];
                     }
-                    dot[e & 1][o] = XOp<XT>::mfma(xq[e & 1][k][h], u32x4{op[w], op[w + 1], op[w + 2], op[w + 3]}, c);
+                    dot[e & 1][o] = XOp<XT>::mfma(xq[e & 1][k][h], op[b][h], c);
                 }
                 if constexpr (e > 0) {
                     // the m-th share of the piece before
@@ -815,7 +766,7 @@ __global__ __launch_bounds__(kTileThreads, (TileShape<F, XT, TN, KG, SLOT>::kOcc
         });
         if constexpr (U::kSums) {
             // mu times the block sums of x, both blocks of the step in one MFMA
-            const u32x4 mw = min_operand<0>(live ? mu : 0.f);
+            const u32x4 mw = min_operand<0>(mu);
             const u32x4* mx = reinterpret_cast<const u32x4*>(buf + S::kX) + (2 * sc0 + lh) * TN + lr;
 #pragma unroll
             for (int t = 0; t < S::kTS; ++t) acc[t] = XOp<__bf16>::mfma(mx[32 * t], mw, acc[t]);
@@ -826,30 +777,20 @@ __global__ __launch_bounds__(kTileThreads, (TileShape<F, XT, TN, KG, SLOT>::kOcc
     // c - 1, before the barrier that ended it.
     {
         XRegs gx;
+#pragma unroll
+        for (int i = 0; i < S::kXL; ++i) gx.x[i].zero();       // tokens past the tile's stay 0
         load_x(0, gx);
         put_x(0, gx);
         load_x(1, gx);
         __syncthreads();
         for (int s = 0; s < rounds; ++s) {
-            if constexpr (SLOT) {
-                // the slot's last reads are this wave's own: LDS keeps their order
-                SL::put(wreg, slot, W, wown, min(sup_of(s), sups - 1), lane);
-                load_slot(s + 1);
-            }
+            // the slot's last reads are this wave's own: LDS keeps their order
+            put_w();
+            load_w(s + 1);
             static_for(std::make_integer_sequence<int, 4>{}, [&](auto jc) __attribute__((always_inline)) {
                 constexpr int j = decltype(jc)::value;
                 const int c = kParts * s + j / S::kCHS;
-                const uint8_t* buf = lds + (c & 1) * S::kBuf;
-                const int sc0 = S::kCHS * wk + j % S::kCHS;
-                const int n = 4 * s + j;
-                if constexpr (SLOT) {
-                    typename U::Raw r;
-                    SL::take(slot + lr * SL::kPitch, W + wown + (int64_t)min(sup_of(s), sups - 1) * SL::kRow, 2 * j + lh, r);
-                    compute(n, sc0, buf, r);
-                } else {
-                    compute(n, sc0, buf, j & 1 ? r1 : r0);
-                    load_lane(n + 2, j & 1 ? r1 : r0);
-                }
+                compute(jc, s, S::kCHS * wk + j % S::kCHS, lds + (c & 1) * S::kBuf);
                 if constexpr (j % S::kCHS == S::kCHS - 1) {
                     put_x(c + 1, gx);                // past the last chunk: not read
                     load_x(c + 2, gx);
@@ -888,9 +829,9 @@ __global__ __launch_bounds__(kTileThreads, (TileShape<F, XT, TN, KG, SLOT>::kOcc
     }
 }
 
-template <class F, class XT, int TN, int KG, bool SLOT, bool LORA>
+template <class F, class XT, int TN, int KG, bool LORA>
 int32_t launch_tile(const TileCall& c, int plan_tile, hipStream_t st) {
-    using S = TileShape<F, XT, TN, KG, SLOT>;
+    using S = TileShape<F, XT, TN, KG>;
     const int out_rows = c.swiglu ? S::kTM / 2 : S::kTM;
     TileDev d;
     d.W = c.W;
@@ -919,7 +860,7 @@ int32_t launch_tile(const TileCall& c, int plan_tile, hipStream_t st) {
                                  : (c.n_items + TN - 1) / TN;
     if (tiles * d.row_tiles > 0x7fffffff)
         return fail(QMV_EINVAL, "qmv: %lld tiles exceed a launch", (long long)(tiles * d.row_tiles));
-    auto kern = tile_kernel<F, XT, TN, KG, SLOT, LORA>;
+    auto kern = tile_kernel<F, XT, TN, KG, LORA>;
     size_t dyn_max = 0;
     if (const int32_t e = lds_limit(reinterpret_cast<const void*>(kern), kLdsMax, "qmv", &dyn_max)) return e;
     const size_t lds = std::max<size_t>(S::kLds, LORA ? S::kLora : 0);
@@ -928,23 +869,9 @@ int32_t launch_tile(const TileCall& c, int plan_tile, hipStream_t st) {
     return check_launch("qmv");
 }
 
-// Whole lines where the rows are whole pieces of eight blocks on 16 bytes
-// (Q6_K: any; its pieces are 210 bytes) and the lanes' offsets fit 32 bits.
-template <class F>
-bool slots_fit(const TileCall& c) {
-    constexpr int kRow = Slot<F>::kRow;
-    const int64_t matrix_rows = c.swiglu ? 2 * c.rows : c.rows;
-    if (c.cols % 256 || matrix_rows * (c.cols / 256) * kRow > 0xffffffffll) return false;
-    return kRow % 16 != 0 || (aligned(c.W, 16) && c.estride % 16 == 0);
-}
-
 template <class F, class XT, int TN, int KG>
 int32_t launch_tile_s(const TileCall& c, int tile, hipStream_t st) {
-    if (c.lora.rank)
-        return slots_fit<F>(c) ? launch_tile<F, XT, TN, KG, true, true>(c, tile, st)
-                               : launch_tile<F, XT, TN, KG, false, true>(c, tile, st);
-    return slots_fit<F>(c) ? launch_tile<F, XT, TN, KG, true, false>(c, tile, st)
-                           : launch_tile<F, XT, TN, KG, false, false>(c, tile, st);
+    return c.lora.rank ? launch_tile<F, XT, TN, KG, true>(c, tile, st) : launch_tile<F, XT, TN, KG, false>(c, tile, st);
 }
 
 // fp32 activations take three times the LDS and MFMAs: 64 tokens by 256 rows
