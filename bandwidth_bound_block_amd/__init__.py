@@ -167,9 +167,15 @@ def _check(rc):
         raise QmvError(rc, last_error())
 
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _stream(stream):
@@ -461,30 +467,69 @@ class GroupPlan:
         self.buffer, self.n_items, self.n_groups = buffer, n_items, n_groups
 
 
-def _scratch(buf, name, need, like, stream):
-    """A caller's uint8 buffer of at least `need` bytes, or a new one, kept
-    from reuse until a stream other than the current one is done with it."""
+# The calls below run once a layer or a step for a few microseconds of GPU
+# time, so their checks are kept short: one comparison of all that a tensor
+# has to be, and the words for what is wrong only where it is.
+_types = {}          # torch dtype -> x_type, filled at the first call
+_empty = None
+
+
+def _setup():
+    global _empty
     torch = _torch()
-    if buf is None:
-        buf = torch.empty(max(need, 16), dtype=torch.uint8, device=like.device)
-        if stream is not None:
-            buf.record_stream(stream)
-        return buf
-    _dev(buf, name, torch.uint8)
-    if not buf.is_contiguous() or buf.numel() < need:
-        raise ValueError(f"{name} must be contiguous and hold {need} bytes")
-    return buf
+    _types.update(_x_types(torch))
+    _empty = torch.empty
+    return torch
 
 
 def _type_of(t, name):
-    torch = _torch()
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    xt = _x_types(torch).get(t.dtype)
-    if xt is None:
+    """x_type of a float GPU tensor."""
+    if not _types:
+        _setup()
+    xt = _types.get(getattr(t, "dtype", None))
+    if xt is None or not t.is_cuda:
+        torch = _torch()
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a GPU tensor")
         raise ValueError(f"{name} must be float32, float16 or bfloat16 (got {t.dtype})")
-    _dev(t, name, t.dtype)
     return xt
+
+
+def _full(t, name, dtype, shape):
+    """Address of a contiguous GPU tensor of this type and shape."""
+    if getattr(t, "dtype", None) is not dtype or not t.is_cuda or t.shape != shape or not t.is_contiguous():
+        _dev(t, name, dtype)
+        raise ValueError(f"{name} must be a contiguous {list(shape)} tensor")
+    return t.data_ptr()
+
+
+def _bytes_of(t, name, need):
+    """Address of a contiguous uint8 GPU tensor of at least `need` bytes."""
+    if getattr(t, "dtype", None) is not _torch().uint8 or not t.is_cuda or not t.is_contiguous() or t.numel() < need:
+        _dev(t, name, _torch().uint8)
+        raise ValueError(f"{name} must be contiguous and hold {need} bytes")
+    return t.data_ptr()
+
+
+def _scratch(buf, name, need, like, stream):
+    """A caller's uint8 buffer of at least `need` bytes, or a new one, kept
+    from reuse until a stream other than the current one is done with it."""
+    if buf is None:
+        buf = _empty(need or 16, dtype=_torch().uint8, device=like.device)
+        if stream is not None:
+            buf.record_stream(stream)
+    else:
+        _bytes_of(buf, name, need)
+    return buf
+
+
+def _on(stream, t):
+    """The HIP stream of a call: stream's, or the current one of t's device."""
+    if stream is not None:
+        return stream.cuda_stream
+    return _torch()._C._cuda_getCurrentRawStream(t.get_device())
 
 
 def qmv_group_plan(group_ids, n_groups, plan=None, stream=None):
@@ -492,39 +537,35 @@ def qmv_group_plan(group_ids, n_groups, plan=None, stream=None):
     by group and returns the GroupPlan that the grouped products take.  plan:
     a uint8 GPU tensor to build it in (its size: the library's
     qmv_group_plan_bytes), or None for a new one."""
-    torch = _torch()
-    _dev(group_ids, "group_ids", torch.int32)
-    if not group_ids.is_contiguous():
-        raise ValueError("group_ids must be contiguous")
+    torch = _torch() if _types else _setup()
+    ids = _full(group_ids, "group_ids", torch.int32, getattr(group_ids, "shape", None))
     n = group_ids.numel()
     buf = _scratch(plan, "plan", _lib.qmv_group_plan_bytes(n, n_groups), group_ids, stream)
-    _check(_lib.qmv_group_plan(group_ids.data_ptr(), n, n_groups, buf.data_ptr(), buf.numel(), _stream(stream)))
+    _check(_lib.qmv_group_plan(ids, n, n_groups, buf.data_ptr(), buf.numel(), _on(stream, group_ids)))
     return GroupPlan(buf, n, n_groups)
 
 
 def _grouped(cfn, fmt, W, stride, E, rows, matrix_rows, cols, plan, top_k, x, out, name, dtype, stream):
-    torch = _torch()
     f = _fmt(fmt)
-    _dev(W, "W_experts", torch.uint8)
-    if not W.is_contiguous() or W.numel() < (E - 1) * stride + matrix_rows * row_bytes(f, cols):
-        raise ValueError("W_experts must be contiguous and hold n_experts expert matrices")
+    w = _bytes_of(W, "W_experts", (E - 1) * stride + matrix_rows * row_bytes(f, cols))
     xt = _type_of(x, "x")
     if x.dim() == 2 and x.shape[1] == cols and x.stride(1) == 1:
         st_tok, st_slot = x.stride(0), 0
-    elif x.dim() == 3 and tuple(x.shape[1:]) == (top_k, cols) and x.stride(2) == 1:
-        st_tok, st_slot = x.stride(0), x.stride(1)
+    elif x.dim() == 3 and x.shape[1] == top_k and x.shape[2] == cols and x.stride(2) == 1:
+        st_tok, st_slot, _ = x.stride()
     else:
         raise ValueError("x must be [tokens, K] or [tokens, top_k, K] with K = n_cols and unit inner stride")
     T = x.shape[0]
     if not isinstance(plan, GroupPlan) or plan.n_items != T * top_k or plan.n_groups != E:
         raise ValueError(f"plan must be qmv_group_plan's of {T * top_k} items and {E} groups")
     if out is None:
-        out = torch.empty((T, top_k, rows), dtype=dtype or torch.float32, device=x.device)
-    ot = _type_of(out, name)
-    if tuple(out.shape) != (T, top_k, rows) or not out.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous [tokens, top_k, {rows}] tensor")
-    _check(cfn(f, W.data_ptr(), stride, E, rows, cols, plan.buffer.data_ptr(), T, top_k, x.data_ptr(), xt, st_tok,
-               st_slot, out.data_ptr(), ot, _stream(stream)))
+        out = _empty((T, top_k, rows), dtype=dtype or _torch().float32, device=x.device)
+        ot = _type_of(out, name)
+    else:
+        ot = _type_of(out, name)
+        _full(out, name, out.dtype, (T, top_k, rows))
+    _check(cfn(f, w, stride, E, rows, cols, plan.buffer.data_ptr(), T, top_k, x.data_ptr(), xt, st_tok, st_slot,
+               out.data_ptr(), ot, _on(stream, x)))
     return out
 
 
@@ -552,21 +593,19 @@ def qmv_moe_weighted_sum(y, weights, out=None, out_dtype=None, stream=None):
     """out [tokens, n_rows] = sum over the slots of weights[t, s] * y[t, s];
     y float32, float16 or bfloat16 [tokens, top_k, n_rows], weights float32
     [tokens, top_k]."""
-    torch = _torch()
     yt = _type_of(y, "y")
-    _dev(weights, "weights", torch.float32)
+    torch = _torch()
     if y.dim() != 3 or not y.is_contiguous():
         raise ValueError("y must be a contiguous [tokens, top_k, n_rows] tensor")
     T, S, N = y.shape
-    if tuple(weights.shape) != (T, S) or not weights.is_contiguous():
-        raise ValueError("weights must be a contiguous [tokens, top_k] tensor")
+    w = _full(weights, "weights", torch.float32, (T, S))
     if out is None:
-        out = torch.empty((T, N), dtype=out_dtype or torch.float32, device=y.device)
-    ot = _type_of(out, "out")
-    if tuple(out.shape) != (T, N) or not out.is_contiguous():
-        raise ValueError("out must be a contiguous [tokens, n_rows] tensor")
-    _check(_lib.qmv_moe_weighted_sum(y.data_ptr(), yt, weights.data_ptr(), T, S, N, out.data_ptr(), ot,
-                                     _stream(stream)))
+        out = _empty((T, N), dtype=out_dtype or torch.float32, device=y.device)
+        ot = _type_of(out, "out")
+    else:
+        ot = _type_of(out, "out")
+        _full(out, "out", out.dtype, (T, N))
+    _check(_lib.qmv_moe_weighted_sum(y.data_ptr(), yt, w, T, S, N, out.data_ptr(), ot, _on(stream, y)))
     return out
 
 
@@ -579,39 +618,30 @@ def qmv_lora(fmt, W, n_rows, n_cols, x, A, B, scales, adapter_ids, y=None, works
     [adapters]; adapter_ids int32 [tokens].  y is float32 [tokens, n_rows].
     workspace: a uint8 GPU tensor of the library's qmv_lora_workspace_bytes,
     or None for a new one."""
+    xt, at = _type_of(x, "x"), _type_of(A, "A")
     torch = _torch()
     f = _fmt(fmt)
-    _dev(W, "W", torch.uint8)
-    need = n_rows * row_bytes(f, n_cols)
-    if W.numel() < need or not W.is_contiguous():
-        raise ValueError(f"W must be contiguous and hold {need} bytes")
-    xt = _type_of(x, "x")
-    if x.dim() != 2:
-        raise ValueError("x must be [tokens, K]")
-    x2, T, ldx = _rows2d(x, "x", n_cols)
-    at = _type_of(A, "A")
-    _dev(B, "B", A.dtype)
+    w = _bytes_of(W, "W", n_rows * row_bytes(f, n_cols))
+    if x.dim() != 2 or x.shape[1] != n_cols or x.stride(1) != 1:
+        raise ValueError(f"x must be [tokens, K] with K={n_cols} and unit inner stride")
+    T, ldx = x.shape[0], x.stride(0)
     if A.dim() != 3 or A.shape[2] != n_cols or not A.is_contiguous():
         raise ValueError("A must be a contiguous [adapters, rank, K] tensor")
-    G, R = A.shape[0], A.shape[1]
-    if tuple(B.shape) != (G, n_rows, R) or not B.is_contiguous():
-        raise ValueError(f"B must be a contiguous [{G}, {n_rows}, {R}] tensor")
-    _dev(scales, "scales", torch.float32)
-    _dev(adapter_ids, "adapter_ids", torch.int32)
-    if tuple(scales.shape) != (G,) or not scales.is_contiguous():
-        raise ValueError("scales must be a contiguous [adapters] tensor")
-    if tuple(adapter_ids.shape) != (T,) or not adapter_ids.is_contiguous():
-        raise ValueError("adapter_ids must be a contiguous [tokens] tensor")
+    G, R, _ = A.shape
+    b = _full(B, "B", A.dtype, (G, n_rows, R))
+    s = _full(scales, "scales", torch.float32, (G,))
+    ids = _full(adapter_ids, "adapter_ids", torch.int32, (T,))
     if y is None:
-        y = torch.empty((T, n_rows), dtype=torch.float32, device=x.device)
-    _dev(y, "y", torch.float32)
-    y2, Ty, ldy = _rows2d(y, "y", n_rows)
-    if Ty != T:
-        raise ValueError("y must have as many rows as x")
+        y = _empty((T, n_rows), dtype=torch.float32, device=x.device)
+        ldy = n_rows
+    else:
+        _dev(y, "y", torch.float32)
+        y2, Ty, ldy = _rows2d(y, "y", n_rows)
+        if Ty != T:
+            raise ValueError("y must have as many rows as x")
     ws = _scratch(workspace, "workspace", _lib.qmv_lora_workspace_bytes(T, R, G), x, stream)
-    _check(_lib.qmv_lora(f, W.data_ptr(), n_rows, n_cols, x2.data_ptr(), xt, ldx, T, A.data_ptr(), B.data_ptr(), at, G,
-                         R, scales.data_ptr(), adapter_ids.data_ptr(), y2.data_ptr(), ldy, ws.data_ptr(), ws.numel(),
-                         _stream(stream)))
+    _check(_lib.qmv_lora(f, w, n_rows, n_cols, x.data_ptr(), xt, ldx if T > 1 else n_cols, T, A.data_ptr(), b, at, G, R, s,
+                         ids, y.data_ptr(), ldy, ws.data_ptr(), ws.numel(), _on(stream, x)))
     return y
 
 
@@ -626,38 +656,33 @@ def qmv_spec_verify(logits, draft_probs, draft_tokens, n_draft, u_accept, u_last
     n_draft int32 [requests]; u_accept float32 [requests, drafts]; u_last
     float32 [requests].  Returns (tokens int32 [requests, drafts + 1],
     n_kept int32 [requests])."""
-    torch = _torch()
     lt = _type_of(logits, "logits")
+    torch = _torch()
     if logits.dim() != 3 or logits.stride(2) != 1:
         raise ValueError("logits must be [requests, drafts + 1, vocab] with unit inner stride")
     Q, D1, V = logits.shape
     D = D1 - 1
-
-    def flat(t, name, dtype, shape):
-        _dev(t, name, dtype)
-        if tuple(t.shape) != shape or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous {list(shape)} tensor")
-        return t.data_ptr()
+    lr, ll, _ = logits.stride()
+    i32, f32 = torch.int32, torch.float32
     qp, qr, ql = None, 0, 0
     if draft_probs is not None:
-        _dev(draft_probs, "draft_probs", torch.float32)
-        if tuple(draft_probs.shape) != (Q, D, V) or draft_probs.stride(2) != 1:
+        _dev(draft_probs, "draft_probs", f32)
+        if draft_probs.shape != (Q, D, V) or draft_probs.stride(2) != 1:
             raise ValueError("draft_probs must be [requests, drafts, vocab] with unit inner stride")
-        qp, qr, ql = draft_probs.data_ptr(), draft_probs.stride(0), draft_probs.stride(1)
+        qp, (qr, ql, _) = draft_probs.data_ptr(), draft_probs.stride()
+    x, n = _full(draft_tokens, "draft_tokens", i32, (Q, D)), _full(n_draft, "n_draft", i32, (Q,))
+    u, ul = _full(u_accept, "u_accept", f32, (Q, D)), _full(u_last, "u_last", f32, (Q,))
     if tokens is None:
-        tokens = torch.empty((Q, D + 1), dtype=torch.int32, device=logits.device)
+        tokens = _empty((Q, D1), dtype=i32, device=logits.device)
+    else:
+        _full(tokens, "tokens", i32, (Q, D1))
     if n_kept is None:
-        n_kept = torch.empty((Q,), dtype=torch.int32, device=logits.device)
-    ws = _scratch(workspace, "workspace", _lib.qmv_spec_verify_workspace_bytes(Q, D, V), logits,
-                  stream)
-    _check(_lib.qmv_spec_verify(logits.data_ptr(), lt, logits.stride(0), logits.stride(1), qp, qr, ql,
-                                flat(draft_tokens, "draft_tokens", torch.int32, (Q, D)),
-                                flat(n_draft, "n_draft", torch.int32, (Q,)),
-                                flat(u_accept, "u_accept", torch.float32, (Q, D)),
-                                flat(u_last, "u_last", torch.float32, (Q,)), Q, D, V,
-                                flat(tokens, "tokens", torch.int32, (Q, D + 1)),
-                                flat(n_kept, "n_kept", torch.int32, (Q,)), ws.data_ptr(), ws.numel(),
-                                _stream(stream)))
+        n_kept = _empty((Q,), dtype=i32, device=logits.device)
+    else:
+        _full(n_kept, "n_kept", i32, (Q,))
+    ws = _scratch(workspace, "workspace", _lib.qmv_spec_verify_workspace_bytes(Q, D, V), logits, stream)
+    _check(_lib.qmv_spec_verify(logits.data_ptr(), lt, lr, ll, qp, qr, ql, x, n, u, ul, Q, D, V, tokens.data_ptr(),
+                                n_kept.data_ptr(), ws.data_ptr(), ws.numel(), _on(stream, logits)))
     return tokens, n_kept
 
 

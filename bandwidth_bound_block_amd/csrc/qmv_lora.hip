@@ -46,7 +46,8 @@ template <bool F16> struct Piece<float, F16> {
 // v[part][t][r] = scales[a] * sum over the part's columns of A[a][r][k] x[t][k].
 // A workgroup takes 32 tokens and a part of the columns; its four waves take
 // groups of 128 columns in turn, and the sums of an adapter's rows with all
-// 32 tokens are kept for its own tokens.  RT: rank rows in 32s.
+// 32 tokens are kept for its own tokens.  Workgroup z of gridDim.z takes
+// every gridDim.z-th of the adapters among the tokens.  RT: rank rows in 32s.
 template <class XT, class AT, int RT>
 __global__ __launch_bounds__(256) void lora_shrink_kernel(const XT* __restrict__ x, int64_t ldx,
                                                           const AT* __restrict__ A, const float* __restrict__ scales,
@@ -66,10 +67,11 @@ __global__ __launch_bounds__(256) void lora_shrink_kernel(const XT* __restrict__
     const XT* xr = x + tok * ldx + 8 * lh;
     const int64_t K = 32 * (int64_t)nb;
     uint32_t todo = (uint32_t)__ballot(lr < count && (unsigned)id < (unsigned)n_adapters);
-    while (todo) {
+    for (unsigned turn = 0; todo; ++turn) {
         const int ad = __builtin_amdgcn_readlane(id, __builtin_ctz(todo));
         const uint32_t own = (uint32_t)__ballot(id == ad) & todo;
         todo &= ~own;
+        if (turn % gridDim.z != blockIdx.z) continue;
         const AT* ar[RT];
 #pragma unroll
         for (int r = 0; r < RT; ++r) ar[r] = A + ((int64_t)ad * rank + min(32 * r + lr, rank - 1)) * K + 8 * lh;
@@ -179,14 +181,18 @@ struct LoraCall {
 // tokens, and at least one group of 128 columns for every wave.
 int lora_parts(int64_t T, int64_t K) {
     const int64_t tiles = (T + 31) / 32, most = (K + 511) / 512;
-    return (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(16, most), 256 / tiles));
+    return (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(16, most), 128 / tiles));
 }
 
 template <class XT, class AT, int RT>
 int32_t shrink(const LoraCall& c, hipStream_t st) {
     const int xvec = aligned(c.x, 16) && c.ldx % (16 / (int)sizeof(XT)) == 0, avec = aligned(c.A, 16);
-    hipLaunchKernelGGL((lora_shrink_kernel<XT, AT, RT>), dim3((unsigned)((c.T + 31) / 32), (unsigned)c.parts), dim3(256),
-                       0, st, (const XT*)c.x, c.ldx, (const AT*)c.A, c.scales, c.ids, (int)c.T, c.n_adapters, c.rank,
+    const int64_t tiles = (c.T + 31) / 32;
+    // adapters side by side, up to about 1024 workgroups in all
+    const int64_t most = std::min<int64_t>(std::min<int64_t>(32, c.T), c.n_adapters);
+    const unsigned side = (unsigned)std::max<int64_t>(1, std::min<int64_t>(most, 1024 / (tiles * c.parts)));
+    hipLaunchKernelGGL((lora_shrink_kernel<XT, AT, RT>), dim3((unsigned)tiles, (unsigned)c.parts, side), dim3(256), 0, st,
+                       (const XT*)c.x, c.ldx, (const AT*)c.A, c.scales, c.ids, (int)c.T, c.n_adapters, c.rank,
                        (int)(c.K / 32), xvec, avec, c.v);
     return check_launch("qmv_lora");
 }

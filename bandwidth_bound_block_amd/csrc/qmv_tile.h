@@ -30,6 +30,7 @@ namespace {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
@@ -351,7 +352,7 @@ struct TileDev {
     void* y;
     int y_type;
     int64_t ldy;
-    int swiglu, vec;
+    int swiglu, vec, yvec;
     int tiles_at, order_at;
     LoraTile lora;
 };
@@ -364,6 +365,28 @@ __device__ __forceinline__ void store_y(void* y, int y_type, int64_t at, float v
     } else {
         static_cast<__bf16*>(y)[at] = (__bf16)v;
     }
+}
+
+// Up to four neighbouring outputs (`left` of them exist), in one store where
+// every output row is on four elements.
+__device__ __forceinline__ void store_y4(void* y, int y_type, int64_t at, f32x4 v, int left, bool vec) {
+    if (!vec || left < 4) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (k < left) store_y(y, y_type, at + k, v[k]);
+        return;
+    }
+    if (y_type == QMV_X_F32) {
+        *reinterpret_cast<f32x4*>(static_cast<float*>(y) + at) = v;
+        return;
+    }
+    uint32_t w[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+        w[k] = y_type == QMV_X_F16
+                   ? __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{v[2 * k], v[2 * k + 1]}, f16x2))
+                   : __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{v[2 * k], v[2 * k + 1]}, bf16x2));
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(y) + at) = uint2{w[0], w[1]};
 }
 
 constexpr int kTileWaves = 4;
@@ -386,23 +409,33 @@ __device__ __forceinline__ void add_adapters(const LoraTile& l, const int* s_ada
         const int ranks = min(kLoraRanks, l.rank - c0);
         const int steps = (ranks + 15) >> 4;
         __syncthreads();
-        // pairs of ranks, zeros past the last up to whole steps
-        for (int i = tid; i < TN * 8 * steps; i += kTileThreads) {
-            const int j = i / (8 * steps), r = 2 * (i % (8 * steps));
-            float a = 0.f, b = 0.f;
+        // fours of ranks, zeros past the last up to whole steps
+        for (int i = tid; i < TN * 4 * steps; i += kTileThreads) {
+            const int j = i / (4 * steps), r = 4 * (i % (4 * steps));
+            f32x4 x = {0.f, 0.f, 0.f, 0.f};
             if (j < count) {
                 const float* v = l.v + (int64_t)(first + j) * l.rank + c0 + r;
-                for (int p = 0; p < l.parts; ++p, v += (int64_t)n_items * l.rank) {
-                    if (r < ranks) a += v[0];
-                    if (r + 1 < ranks) b += v[1];
+                if (l.rank % 4 == 0) {
+                    if (r < ranks)
+                        for (int p = 0; p < l.parts; ++p)
+                            x += *reinterpret_cast<const f32x4*>(v + (int64_t)p * n_items * l.rank);
+                } else {
+                    for (int p = 0; p < l.parts; ++p)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            if (r + k < ranks) x[k] += v[(int64_t)p * n_items * l.rank + k];
                 }
             }
 #pragma unroll
             for (int k = 0; k < 3; ++k) {
-                const uint32_t w = __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{a, b}, bf16x2));
-                *reinterpret_cast<uint32_t*>(lds + (k * TN + j) * kLoraPitch + 2 * r) = w;
-                a -= __builtin_bit_cast(float, w << 16);
-                b -= __builtin_bit_cast(float, w & 0xffff0000u);
+                uint32_t w[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    w[e] = __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{x[2 * e], x[2 * e + 1]}, bf16x2));
+                    x[2 * e] -= __builtin_bit_cast(float, w[e] << 16);
+                    x[2 * e + 1] -= __builtin_bit_cast(float, w[e] & 0xffff0000u);
+                }
+                *reinterpret_cast<uint2*>(lds + (k * TN + j) * kLoraPitch + 2 * r) = uint2{w[0], w[1]};
             }
         }
         __syncthreads();
@@ -526,6 +559,7 @@ __global__ __launch_bounds__(kTileThreads, (TileShape<F, XT, TN, KG>::kOcc)) voi
     using U = Unit<F>;
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
     __shared__ int s_item[TN], s_adapter[LORA ? TN : 1];
+    __shared__ int64_t s_x[TN];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
 
@@ -612,7 +646,10 @@ __global__ __launch_bounds__(kTileThreads, (TileShape<F, XT, TN, KG>::kOcc)) voi
 
     if (tid < TN) {
         const int at = start + min(tid, count - 1);
-        s_item[tid] = a.plan ? a.plan[a.order_at + at] : at;
+        const int item = a.plan ? a.plan[a.order_at + at] : at;
+        const int tok = a.top_k == 1 ? item : item / a.top_k;
+        s_item[tid] = item;
+        s_x[tid] = tok * a.xs_tok + (item - tok * a.top_k) * a.xs_slot;
         if constexpr (LORA) s_adapter[tid] = a.lora.ids[at];
     }
     __syncthreads();
@@ -634,8 +671,7 @@ __global__ __launch_bounds__(kTileThreads, (TileShape<F, XT, TN, KG>::kOcc)) voi
     const XT* xp[S::kXL];
 #pragma unroll
     for (int i = 0; i < S::kXL; ++i) {
-        const int p = s_item[xt + kXStep * i];
-        xp[i] = static_cast<const XT*>(a.x) + (int64_t)(p / a.top_k) * a.xs_tok + (int64_t)(p % a.top_k) * a.xs_slot;
+        xp[i] = static_cast<const XT*>(a.x) + s_x[xt + kXStep * i];
     }
     const bool vec = a.vec != 0;
     struct XRegs {
@@ -812,20 +848,26 @@ __global__ __launch_bounds__(kTileThreads, (TileShape<F, XT, TN, KG>::kOcc)) voi
         for (int i = 0; i < 16; ++i)
             out[(wk * TN + 32 * t + 8 * (i >> 2) + 4 * lh + (i & 3)) * S::kOutPitch + wr + lr] = acc[t][i];
     __syncthreads();
-    auto result = [&](int j, int r) __attribute__((always_inline)) {
-        float v = out[j * S::kOutPitch + r];
+    // four rows a thread; rows of a tile are a power of two
+    const int quads = out_rows >> 2, qshift = __builtin_ctz(quads);
+    for (int i = tid; i < count << qshift; i += kTileThreads) {
+        const int j = i >> qshift, r = (i & (quads - 1)) << 2;
+        auto result = [&](int rr) __attribute__((always_inline)) {
+            f32x4 v = *reinterpret_cast<const f32x4*>(out + j * S::kOutPitch + rr);
 #pragma unroll
-        for (int k = 1; k < KG; ++k) v += out[(k * TN + j) * S::kOutPitch + r];
-        return v;
-    };
-    for (int i = tid; i < count * out_rows; i += kTileThreads) {
-        const int j = i / out_rows, r = i % out_rows;
-        if (row0 + r >= a.rows) continue;
-        float v = result(j, r);
-        if (a.swiglu) v = silu(v) * result(j, out_rows + r);
-        if constexpr (LORA)
-            if (s_adapter[j] < -1 || s_adapter[j] >= a.lora.n_adapters) v = __builtin_nanf("");
-        store_y(a.y, a.y_type, (int64_t)s_item[j] * a.ldy + row0 + r, v);
+            for (int k = 1; k < KG; ++k) v += *reinterpret_cast<const f32x4*>(out + (k * TN + j) * S::kOutPitch + rr);
+            return v;
+        };
+        f32x4 v = result(r);
+        if (a.swiglu) {
+            const f32x4 u = result(out_rows + r);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v[k] = silu(v[k]) * u[k];
+        }
+        if constexpr (LORA) {
+            if (s_adapter[j] < -1 || s_adapter[j] >= a.lora.n_adapters) v = f32x4{1.f, 1.f, 1.f, 1.f} * __builtin_nanf("");
+        }
+        store_y4(a.y, a.y_type, (int64_t)s_item[j] * a.ldy + row0 + r, v, a.rows - row0 - r, a.yvec != 0);
     }
 }
 
@@ -851,6 +893,7 @@ int32_t launch_tile(const TileCall& c, int plan_tile, hipStream_t st) {
     d.y_type = c.y_type;
     d.ldy = c.ldy;
     d.swiglu = c.swiglu;
+    d.yvec = c.ldy % 4 == 0 && aligned(c.y, c.y_type == QMV_X_F32 ? 16 : 8);
     const int per16 = 16 / (int)sizeof(XT);
     d.vec = aligned(c.x, 16) && c.xs_tok % per16 == 0 && c.xs_slot % per16 == 0;
     d.tiles_at = (int)plan_tiles_at(c.n_groups);
@@ -886,12 +929,7 @@ int32_t launch_tile_n(const TileCall& c, hipStream_t st) {
     const int64_t matrix_rows = c.swiglu ? 2 * c.rows : c.rows;
     const int64_t wide = groups * ((c.n_items / groups + kWide - 1) / kWide) * ((matrix_rows + 127) / 128);
     if (tile == 128 && wide >= device_cu_count()) return launch_tile_s<F, XT, kWide, 1>(c, tile, st);
-    if (const char* e = getenv("KG")) {   // TEMP
-        const int kg = atoi(e);
-        if constexpr (!std::is_same<XT, float>::value) if (kg == 4) return launch_tile_s<F, XT, 32, 4>(c, tile, st);
-        if (kg == 2) return launch_tile_s<F, XT, 32, 2>(c, tile, st);
-        if (kg == 1) return launch_tile_s<F, XT, 32, 1>(c, tile, st);
-    }
+    if (tile == 128) return launch_tile_s<F, XT, 64, std::is_same<XT, float>::value ? 2 : 4>(c, tile, st);
     const int64_t waves = groups * ((c.n_items / groups + 31) / 32) * ((matrix_rows + 31) / 32);
     if constexpr (!std::is_same<XT, float>::value)
         if (waves < 4 * device_cu_count() && !c.swiglu) return launch_tile_s<F, XT, 32, 4>(c, tile, st);

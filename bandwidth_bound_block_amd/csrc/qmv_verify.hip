@@ -10,8 +10,11 @@
 // target's own.
 //
 // Three launches: (1) every row's maximum and sum of exponentials, in chunks
-// of the vocabulary; (2) the decisions, and the chunk sums of the drawn row's
-// weights; (3) the chunk and the place in it.  Exponentials and sums are in
+// of the vocabulary; (2) the decisions, made alike by every workgroup of a
+// request, and the chunk sums of the drawn row's weights; (3) the chunk and
+// the place in it.  (3) by the last workgroup of (2) took longer: the fences
+// it needs write the L2s back (139 us against 26 + 27 for 64 requests of
+// 151936 tokens).  Exponentials and sums are in
 // fp64: the outputs are comparisons, and with fp32 sums (1e-7 off) over a
 // vocabulary of 1.5e5 about one draw in thirty could fall on the wrong side
 // of a border between two tokens of mean mass.
@@ -23,11 +26,13 @@
 namespace qmv {
 namespace {
 
+struct Decision;
 constexpr int kVT = 256;                 // threads
 constexpr int kVWaves = kVT / 64;
 constexpr int kVPer = 16;                // logits a thread holds
 constexpr int kVChunk = kVT * kVPer;     // logits of a workgroup
 constexpr int kVDrafts = 64;             // most drafted tokens of a request
+constexpr int kVMaxChunks = 1024;        // most chunks of a vocabulary
 
 struct VerifyArgs {
     const void* logits;
@@ -41,23 +46,21 @@ struct VerifyArgs {
     int D, V, chunks, vec, qvec;
     double2* part;         // [requests][D + 1][chunks]: maximum, sum of exp(l - maximum)
     double2* sums;         // [requests][chunks]: sum of max(p - q, 0), sum of p, times the row's sum
+    Decision* made; // [requests]
     int32_t* tokens;
     int32_t* kept;
 };
 
 __device__ __forceinline__ int drafts_of(const VerifyArgs& a, int r) { return min(max(a.n_draft[r], 0), a.D); }
 
-// e^x for x <= 0 to about 1e-14: x = n ln 2 + f, |f| <= ln 2 / 2, the Taylor
-// polynomial of degree 11 (its remainder f^12 / 12! < 7e-15), times 2^n.
-// Below -700 the value is 0 beside a row's largest term, 1; NaN stays NaN.
+// e^x for x <= 0 to about 7e-12: x = n ln 2 + f, |f| <= ln 2 / 2, the Taylor
+// polynomial of degree 9 (its remainder f^10 / 10!), times 2^n; over 1.5e5
+// tokens that leaves a draw off the exact one about once in 1e6.  Below -700
+// the value is 0 beside a row's largest term, 1; NaN stays NaN.
 __device__ __forceinline__ double exp_neg(double x) {
-    if (x < -700.0) return 0.0;
     const double n = __builtin_rint(x * 1.4426950408889634074);
-    double f = __builtin_fma(n, -0x1.62e42fefa39efp-1, x);      // ln 2 rounded to fp64
-    f = __builtin_fma(n, -0x1.abc9e3b39803fp-56, f);            // and what that leaves
-    double p = 1.0 / 39916800.0;
-    p = __builtin_fma(p, f, 1.0 / 3628800.0);
-    p = __builtin_fma(p, f, 1.0 / 362880.0);
+    const double f = __builtin_fma(n, -0x1.62e42fefa39efp-1, x);
+    double p = 1.0 / 362880.0;
     p = __builtin_fma(p, f, 1.0 / 40320.0);
     p = __builtin_fma(p, f, 1.0 / 5040.0);
     p = __builtin_fma(p, f, 1.0 / 720.0);
@@ -67,7 +70,8 @@ __device__ __forceinline__ double exp_neg(double x) {
     p = __builtin_fma(p, f, 0.5);
     p = __builtin_fma(p, f, 1.0);
     p = __builtin_fma(p, f, 1.0);
-    return __builtin_ldexp(p, (int)n);
+    p = __builtin_ldexp(p, (int)n);
+    return x < -700.0 ? 0.0 : p;
 }
 
 __device__ __forceinline__ double wave_sum(double s) {
@@ -81,21 +85,25 @@ __device__ __forceinline__ float wave_max(float m) {
     return m;
 }
 
+// Elements v..v+3 of a row; those past its end are `pad`.
+template <class LT>
+__device__ __forceinline__ void load_quad(const LT* p, int v, int V, bool vec, float pad, float* f) {
+    if (vec && v + 3 < V) {
+        const float4 w = XIn<LT>::load4(p + v);
+        f[0] = w.x; f[1] = w.y; f[2] = w.z; f[3] = w.w;
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) f[j] = v + j < V ? XIn<LT>::load1(p + v + j) : pad;
+    }
+}
+
 // Quads of a chunk: thread t holds elements 4 (t + 256 k) .. + 3, k < 4, so
 // that a wave's loads run along the row.  Elements past the row are `pad`.
 template <class LT>
 __device__ __forceinline__ void load_chunk(const LT* p, int v0, int V, bool vec, float pad, float (&f)[kVPer]) {
 #pragma unroll
-    for (int k = 0; k < kVPer / 4; ++k) {
-        const int v = v0 + 4 * ((int)threadIdx.x + kVT * k);
-        if (vec && v + 3 < V) {
-            const float4 w = XIn<LT>::load4(p + v);
-            f[4 * k] = w.x; f[4 * k + 1] = w.y; f[4 * k + 2] = w.z; f[4 * k + 3] = w.w;
-        } else {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) f[4 * k + j] = v + j < V ? XIn<LT>::load1(p + v + j) : pad;
-        }
-    }
+    for (int k = 0; k < kVPer / 4; ++k)
+        load_quad<LT>(p, v0 + 4 * ((int)threadIdx.x + kVT * k), V, vec, pad, f + 4 * k);
 }
 
 // (1) maximum and sum of a chunk of a row
@@ -146,7 +154,8 @@ struct Decision {
 // or 0, and no comparison with it holds.
 template <class LT>
 __device__ __forceinline__ Decision decide(const VerifyArgs& a, int r) {
-    __shared__ double rm[kVDrafts + 1], rs[kVDrafts + 1];
+    __shared__ double rm[kVDrafts + 1], rs[kVDrafts + 1], rp[kVDrafts], rl[kVDrafts];
+    __shared__ int rx[kVDrafts];
     const int n = drafts_of(a, r);
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     for (int i = wave; i <= n; i += kVWaves) {
@@ -166,28 +175,44 @@ __device__ __forceinline__ Decision decide(const VerifyArgs& a, int r) {
             rs[i] = s;
         }
     }
-    __syncthreads();
-    Decision d;
-    d.x = -1;
-    d.all = true;
-    int i = 0;
-    for (; i < n; ++i) {
-        const int x = a.drafted[(int64_t)r * a.D + i];
-        bool keep = false;
-        if ((unsigned)x < (unsigned)a.V) {
-            const float l = XIn<LT>::load1(static_cast<const LT*>(a.logits) + r * a.ls_req + i * a.ls_row + x);
-            const float qx = a.q ? a.q[r * a.qs_req + i * a.qs_row + x] : 1.f;
-            keep = (double)a.u[(int64_t)r * a.D + i] * (double)qx * rs[i] < exp_neg((double)l - rm[i]);
+    // token i by thread i; the first that is not kept ends them
+    __shared__ int s_kept, s_x;
+    if (threadIdx.x < 64) {
+        bool keep = true;
+        int x = -1;
+        if (lane < n) {
+            x = a.drafted[(int64_t)r * a.D + lane];
+            keep = false;
+            if ((unsigned)x < (unsigned)a.V) {
+                const float l = XIn<LT>::load1(static_cast<const LT*>(a.logits) + r * a.ls_req + lane * a.ls_row + x);
+                const float qx = a.q ? a.q[r * a.qs_req + lane * a.qs_row + x] : 1.f;
+                const float u = a.u[(int64_t)r * a.D + lane];
+                rp[lane] = (double)u * (double)qx;
+                rl[lane] = (double)l;
+                keep = true;
+            } else {
+                x = -1;
+            }
         }
-        if (!keep) {
-            d.all = false;
-            if (!a.q && (unsigned)x < (unsigned)a.V) d.x = x;
-            break;
+        rx[lane] = keep ? x : -1;
+    }
+    __syncthreads();
+    if (threadIdx.x < 64) {
+        bool keep = lane >= n || rx[lane] >= 0;
+        if (lane < n && keep) keep = rp[lane] * rs[lane] < exp_neg(rl[lane] - rm[lane]);
+        const uint64_t no = __ballot(!keep);
+        if (lane == 0) {
+            s_kept = no ? __builtin_ctzll(no) : n;
+            s_x = !a.q && no ? rx[s_kept] : -1;
         }
     }
-    d.kept = i;
-    d.m = rm[i];
-    d.s = rs[i];
+    __syncthreads();
+    Decision d;
+    d.kept = s_kept;
+    d.all = d.kept == n;
+    d.x = s_x;
+    d.m = rm[d.kept];
+    d.s = rs[d.kept];
     return d;
 }
 
@@ -226,47 +251,73 @@ __global__ __launch_bounds__(kVT) void verify_weights_kernel(const VerifyArgs a)
     sp = wave_sum(sp);
     if (lane == 0) w[wave] = double2{sl, sp};
     __syncthreads();
-    if (threadIdx.x == 0)
+    if (threadIdx.x == 0) {
         a.sums[(int64_t)r * a.chunks + c] =
             double2{(w[0].x + w[1].x) + (w[2].x + w[3].x), (w[0].y + w[1].y) + (w[2].y + w[3].y)};
+        if (c == 0) a.made[r] = d;
+    }
 }
 
 // (3) the token drawn, and the outputs of request r
 template <class LT>
 __global__ __launch_bounds__(kVT) void verify_draw_kernel(const VerifyArgs a) {
-    const int r = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const Decision d = decide<LT>(a, r);
+    const int r = blockIdx.x;
+    const Decision d = a.made[r];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     __shared__ int s_chunk, s_whole, s_token;
-    __shared__ double s_before, s_goal, wsum[kVWaves];
-    if (tid == 0) {
-        const double2* p = a.sums + (int64_t)r * a.chunks;
+    __shared__ double s_before, s_goal, wsum[kVWaves], cl[kVMaxChunks], cp[kVMaxChunks];
+    const double2* sums = a.sums + (int64_t)r * a.chunks;
+    for (int c = tid; c < a.chunks; c += kVT) {
+        cl[c] = sums[c].x;
+        cp[c] = sums[c].y;
+    }
+    __syncthreads();
+    if (wave == 0) {
+        // each lane a run of chunks; totals and places by scans over the lanes
+        const int per = (a.chunks + 63) / 64, c0 = min(lane * per, a.chunks), c1 = min(c0 + per, a.chunks);
         double tl = 0.0, tp = 0.0;
-        for (int c = 0; c < a.chunks; ++c) {
-            tl += p[c].x;
-            tp += p[c].y;
+        for (int c = c0; c < c1; ++c) {
+            tl += cl[c];
+            tp += cp[c];
         }
+        const double all_left = wave_sum(tl), all_p = wave_sum(tp);
         // p = q leaves nothing: the draw is from p
-        const bool whole = !(tl > 0.0);
-        const double total = whole ? tp : tl;
+        const bool whole = !(all_left > 0.0);
+        const double total = whole ? all_p : all_left, own = whole ? tp : tl;
         const double goal = (double)a.u_last[r] * total;
-        double before = 0.0, at = 0.0;
-        int chunk = -1;
-        if (total > 0.0 && total < (double)__builtin_inff() && d.s > 0.0) {
-            for (int c = 0; c < a.chunks; ++c) {
-                const double w = whole ? p[c].y : p[c].x;
-                if (w > 0.0) {             // the last chunk with weight, if rounding passes them all
-                    chunk = c;
+        double at = own;
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) {
+            const double t = __shfl_up(at, o);
+            if (lane >= o) at += t;
+        }
+        at -= own;
+        // the first chunk that passes the goal, and the last with weight if
+        // rounding passes them all
+        int found = -1, last = -1;
+        double before = 0.0, before_last = 0.0;
+        for (int c = c0; c < c1; ++c) {
+            const double w = whole ? cp[c] : cl[c];
+            if (w > 0.0) {
+                last = c;
+                before_last = at;
+                if (found < 0 && at + w > goal) {
+                    found = c;
                     before = at;
                 }
-                at += w;
-                if (at > goal) break;
             }
+            at += w;
         }
-        s_chunk = chunk;
-        s_whole = whole;
-        s_before = before;
-        s_goal = goal;
-        s_token = -1;
+        const uint64_t f = __ballot(found >= 0), l = __ballot(last >= 0);
+        const bool any = total > 0.0 && total < (double)__builtin_inff() && d.s > 0.0 && l != 0;
+        const int who = f ? __builtin_ctzll(f) : (l ? 63 - __builtin_clzll(l) : 0);
+        if (lane == who) {
+            s_chunk = any ? (f ? found : last) : -1;
+            s_before = f ? before : before_last;
+            s_goal = goal;
+            s_whole = whole;
+            s_token = -1;
+        }
     }
     __syncthreads();
     if (s_chunk >= 0) {
@@ -275,14 +326,16 @@ __global__ __launch_bounds__(kVT) void verify_draw_kernel(const VerifyArgs a) {
         const LT* l = static_cast<const LT*>(a.logits) + r * a.ls_req + d.kept * a.ls_row;
         const float* q = a.q && !d.all ? a.q + r * a.qs_req + d.kept * a.qs_row : nullptr;
         double w[kVPer], own = 0.0;
+        float f[kVPer], g[kVPer];
+#pragma unroll
+        for (int k = 0; k < kVPer; k += 4) {
+            load_quad<LT>(l, v0 + k, a.V, a.vec, -__builtin_inff(), f + k);
+            if (q) load_quad<float>(q, v0 + k, a.V, a.qvec, 0.f, g + k);
+        }
 #pragma unroll
         for (int i = 0; i < kVPer; ++i) {
-            const int v = v0 + i;
-            w[i] = 0.0;
-            if (v < a.V) {
-                const double p = exp_neg((double)XIn<LT>::load1(l + v) - d.m);
-                w[i] = s_whole ? p : left_of(d, p, q ? q[v] : 0.f, v);
-            }
+            const double p = exp_neg((double)f[i] - d.m);
+            w[i] = s_whole ? p : left_of(d, p, q ? g[i] : 0.f, v0 + i);
             own += w[i];
         }
         double in = own;                    // inclusive scan over the threads
@@ -334,6 +387,7 @@ int32_t launch_verify(const VerifyArgs& a, int requests, hipStream_t st) {
 }
 
 constexpr int64_t kVRequests = 65535, kVVocab = 1 << 22;
+static_assert(kVVocab / kVChunk <= kVMaxChunks, "a request's chunk sums fit LDS");
 bool sizes_ok(int64_t requests, int32_t drafts, int64_t vocab) {
     return requests >= 1 && requests <= kVRequests && drafts >= 1 && drafts <= kVDrafts && vocab >= 1 && vocab <= kVVocab;
 }
@@ -345,7 +399,7 @@ int64_t chunks_of(int64_t vocab) { return (vocab + kVChunk - 1) / kVChunk; }
 extern "C" size_t qmv_spec_verify_workspace_bytes(int64_t n_requests, int32_t max_drafts, int64_t vocab) {
     using namespace qmv;
     if (!sizes_ok(n_requests, max_drafts, vocab)) return 0;
-    return (size_t)(n_requests * (max_drafts + 2) * chunks_of(vocab)) * 16;
+    return (size_t)(n_requests * (max_drafts + 2) * chunks_of(vocab)) * 16 + (size_t)n_requests * sizeof(Decision);
 }
 
 extern "C" int32_t qmv_spec_verify(const void* logits, int32_t logits_type, int64_t logits_stride_request,
@@ -392,6 +446,7 @@ extern "C" int32_t qmv_spec_verify(const void* logits, int32_t logits_type, int6
     a.qvec = aligned(draft_probs, 16) && a.qs_req % 4 == 0 && a.qs_row % 4 == 0;
     a.part = static_cast<double2*>(workspace);
     a.sums = a.part + n_requests * (max_drafts + 1) * a.chunks;
+    a.made = reinterpret_cast<Decision*>(a.sums + n_requests * a.chunks);
     a.tokens = tokens;
     a.kept = n_kept;
     const hipStream_t st = as_stream(stream);
