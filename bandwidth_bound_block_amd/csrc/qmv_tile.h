@@ -84,27 +84,28 @@ template <> struct XOp<_Float16> {
 // is read.
 //
 // Unit<F> is a format's step of two blocks, 2 J and 2 J + 1 of the eight (J
-// 0..3), of the lane's row: lane half lh leaves the codes of each block b
-// that MFMA h takes from it, elements at(h, lh) .. + 7, as signed bytes
-// q[b][h][0..1], the blocks' scales d[b][.] (one, or one per 16 weights), and
-// mu of block 2 J + lh.
+// 0..3), of the lane's row, in three parts, so that a step can be decoded
+// bit by bit among the MFMAs of the step before it: read() takes its words
+// from the slot; scales() gives the blocks' scales d[b][.] (one, or one per
+// 16 weights), mu of block 2 J + lh, and what codes() needs; codes() gives
+// the codes of block b that MFMA h takes from lane half lh, elements
+// at(h, lh) .. + 7, as signed bytes.
 //   kRow    bytes of eight blocks;  kCpr  pieces of a row;  kPitch  bytes of
 //   a slot's row, an odd number of 16-byte units.
 template <class F> struct Unit;
 
 __device__ __forceinline__ uint32_t lds4(const uint8_t* p) { return *reinterpret_cast<const uint32_t*>(p); }
-__device__ __forceinline__ float lds_half(const uint8_t* p) {
-    return half_bits_to_float(*reinterpret_cast<const uint16_t*>(p));
-}
-// N words from p, p 0 or 2 (sh) bytes past a word
+__device__ __forceinline__ uint16_t lds2(const uint8_t* p) { return *reinterpret_cast<const uint16_t*>(p); }
+// The words that hold N - 1 words from p, p 0 or 2 (sh) bytes past a word,
+// and the i-th of those.
 template <int N>
-__device__ __forceinline__ void lds_words(const uint8_t* p, uint32_t sh, uint32_t (&w)[N]) {
-    const uint8_t* a = p - sh;
-    uint32_t v[N + 1];
+__device__ __forceinline__ void lds_span(const uint8_t* p, uint32_t sh, uint32_t (&w)[N]) {
 #pragma unroll
-    for (int i = 0; i <= N; ++i) v[i] = lds4(a + 4 * i);
-#pragma unroll
-    for (int i = 0; i < N; ++i) w[i] = __builtin_amdgcn_alignbyte(v[i + 1], v[i], sh);
+    for (int i = 0; i < N; ++i) w[i] = lds4(p - sh + 4 * i);
+}
+template <int N>
+__device__ __forceinline__ uint32_t word_of(const uint32_t (&w)[N], int i, uint32_t sh) {
+    return __builtin_amdgcn_alignbyte(w[i + 1], w[i], sh);
 }
 // Exchanges the upper 32 lanes of a with the lower 32 of b.
 __device__ __forceinline__ void swap_halves(uint32_t& a, uint32_t& b) {
@@ -137,17 +138,28 @@ template <> struct Unit<Q8_0> {
     static constexpr int kSub = 1, kRow = 272, kCpr = 18, kPitch = 304;
     static constexpr bool kSums = false;
     __device__ static constexpr int at(int h, int lh) { return 16 * lh + 8 * h; }
+    struct Raw {
+        uint32_t w[2][5];
+        uint16_t d[2];
+    };
     template <int J>
-    __device__ static void step(const uint8_t* row, uint32_t sh, int lh, uint32_t (&q)[2][2][2], float (&d)[2][kSub],
-                                float&) {
+    __device__ static void read(const uint8_t* row, uint32_t sh, int lh, Raw& r) {
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
             const uint8_t* blk = row + sh + 34 * (2 * J + b);     // 2 b (mod 4) past sh
-            uint32_t w[4];
-            lds_words<4>(blk + 2 + 16 * lh, (sh + 2 * b + 2) & 2, w);
-            q[b][0][0] = w[0]; q[b][0][1] = w[1]; q[b][1][0] = w[2]; q[b][1][1] = w[3];
-            d[b][0] = lds_half(blk);
+            lds_span(blk + 2 + 16 * lh, (sh + 2 * b + 2) & 2, r.w[b]);
+            r.d[b] = lds2(blk);
         }
+    }
+    template <int J>
+    __device__ static void scales(const Raw& r, uint32_t, int, float (&d)[2][kSub], float&, uint32_t (&)[2]) {
+#pragma unroll
+        for (int b = 0; b < 2; ++b) d[b][0] = half_bits_to_float(r.d[b]);
+    }
+    template <int J>
+    __device__ static void codes(const Raw& r, uint32_t sh, int b, int h, const uint32_t (&)[2], uint32_t (&q)[2]) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) q[i] = word_of(r.w[b], 2 * h + i, (sh + 2 * b + 2) & 2);
     }
 };
 
@@ -155,18 +167,31 @@ template <> struct Unit<Q4_0> {
     static constexpr int kSub = 1, kRow = 144, kCpr = 10, kPitch = 176;
     static constexpr bool kSums = false;
     __device__ static constexpr int at(int h, int lh) { return 16 * h + 8 * lh; }
-    // 16 (c - 8) as signed bytes; d / 16 is exact
+    struct Raw {
+        uint32_t w[2][3];
+        uint16_t d[2];
+    };
     template <int J>
-    __device__ static void step(const uint8_t* row, uint32_t sh, int lh, uint32_t (&q)[2][2][2], float (&d)[2][kSub],
-                                float&) {
+    __device__ static void read(const uint8_t* row, uint32_t sh, int lh, Raw& r) {
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
             const uint8_t* blk = row + sh + 18 * (2 * J + b);     // 2 b (mod 4) past sh
-            uint32_t w[2];
-            lds_words<2>(blk + 2 + 8 * lh, (sh + 2 * b + 2) & 2, w);
+            lds_span(blk + 2 + 8 * lh, (sh + 2 * b + 2) & 2, r.w[b]);
+            r.d[b] = lds2(blk);
+        }
+    }
+    // codes are 16 (c - 8); d / 16 is exact
+    template <int J>
+    __device__ static void scales(const Raw& r, uint32_t, int, float (&d)[2][kSub], float&, uint32_t (&)[2]) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i) signed_nibbles(w[i], q[b][0][i], q[b][1][i]);
-            d[b][0] = lds_half(blk) * 0.0625f;
+        for (int b = 0; b < 2; ++b) d[b][0] = half_bits_to_float(r.d[b]) * 0.0625f;
+    }
+    template <int J>
+    __device__ static void codes(const Raw& r, uint32_t sh, int b, int h, const uint32_t (&)[2], uint32_t (&q)[2]) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const uint32_t c = word_of(r.w[b], i, (sh + 2 * b + 2) & 2);
+            q[i] = ((h ? c : c << 4) ^ 0x80808080u) & 0xf0f0f0f0u;
         }
     }
 };
@@ -175,24 +200,29 @@ template <> struct Unit<Q4_1> {
     static constexpr int kSub = 1, kRow = 160, kCpr = 10, kPitch = 176;
     static constexpr bool kSums = true;
     __device__ static constexpr int at(int h, int lh) { return 16 * h + 8 * lh; }
+    struct Raw {
+        uint32_t w[2][2], dm;
+    };
     template <int J>
-    __device__ static void step(const uint8_t* row, uint32_t, int lh, uint32_t (&q)[2][2][2], float (&d)[2][kSub],
-                                float& mu) {
-        const uint32_t dm = lds4(row + 20 * (2 * J + lh));
-        const float D = half_bits_to_float(dm), m = half_bits_to_float(dm >> 16);
-        const float k = pivot(D, -m);
-        mu = __builtin_fmaf(D, k, m);
-        uint32_t k4[2];
-        both_halves((uint32_t)k * 0x01010101u, k4[0], k4[1]);
-        both_halves(D, d[0][0], d[1][0]);
+    __device__ static void read(const uint8_t* row, uint32_t, int lh, Raw& r) {
+        r.dm = lds4(row + 20 * (2 * J + lh));
 #pragma unroll
         for (int b = 0; b < 2; ++b)
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const uint32_t c = lds4(row + 20 * (2 * J + b) + 4 + 8 * lh + 4 * i);
-                q[b][0][i] = less_pivot(c & 0x0f0f0f0fu, k4[b]);
-                q[b][1][i] = less_pivot((c >> 4) & 0x0f0f0f0fu, k4[b]);
-            }
+            for (int i = 0; i < 2; ++i) r.w[b][i] = lds4(row + 20 * (2 * J + b) + 4 + 8 * lh + 4 * i);
+    }
+    template <int J>
+    __device__ static void scales(const Raw& r, uint32_t, int, float (&d)[2][kSub], float& mu, uint32_t (&k4)[2]) {
+        const float D = half_bits_to_float(r.dm), m = half_bits_to_float(r.dm >> 16);
+        const float k = pivot(D, -m);
+        mu = __builtin_fmaf(D, k, m);
+        both_halves((uint32_t)k * 0x01010101u, k4[0], k4[1]);
+        both_halves(D, d[0][0], d[1][0]);
+    }
+    template <int J>
+    __device__ static void codes(const Raw& r, uint32_t, int b, int h, const uint32_t (&k4)[2], uint32_t (&q)[2]) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) q[i] = less_pivot((h ? r.w[b][i] >> 4 : r.w[b][i]) & 0x0f0f0f0fu, k4[b]);
     }
 };
 
@@ -202,27 +232,31 @@ template <> struct Unit<Q4KTile> {
     static constexpr int kSub = 1, kRow = 144, kCpr = 9, kPitch = 144;
     static constexpr bool kSums = true;
     __device__ static constexpr int at(int h, int lh) { return 16 * lh + 8 * h; }
+    struct Raw {
+        u32x4 head, c;
+    };
     template <int J>
-    __device__ static void step(const uint8_t* row, uint32_t, int lh, uint32_t (&q)[2][2][2], float (&d)[2][kSub],
-                                float& mu) {
-        const u32x4 hd = *reinterpret_cast<const u32x4*>(row);
+    __device__ static void read(const uint8_t* row, uint32_t, int lh, Raw& r) {
+        r.head = *reinterpret_cast<const u32x4*>(row);
+        r.c = *reinterpret_cast<const u32x4*>(row + 16 + 32 * J + 16 * lh);
+    }
+    template <int J>
+    __device__ static void scales(const Raw& r, uint32_t, int lh, float (&d)[2][kSub], float& mu, uint32_t (&k4)[2]) {
         const int t = 8 * ((2 * J & 3) + lh);                 // block 2 J + lh: byte J % 4 of the fields
-        const uint32_t h1 = hd.y >> t, h2 = hd.z >> t, h3 = hd.w >> t;
+        const uint32_t h1 = r.head.y >> t, h2 = r.head.z >> t, h3 = r.head.w >> t;
         const uint32_t sc = J < 2 ? (h1 & 63u) : ((h3 & 15u) | ((h1 >> 2) & 48u));
         const uint32_t mn = J < 2 ? (h2 & 63u) : (((h3 >> 4) & 15u) | ((h2 >> 2) & 48u));
-        const float D = half_bits_to_float(hd.x) * (float)sc;          // exact
-        const float M = half_bits_to_float(hd.x >> 16) * (float)mn;    // exact
+        const float D = half_bits_to_float(r.head.x) * (float)sc;          // exact
+        const float M = half_bits_to_float(r.head.x >> 16) * (float)mn;    // exact
         const float k = pivot(D, M);
         mu = __builtin_fmaf(D, k, -M);
-        uint32_t k4[2];
         both_halves((uint32_t)k * 0x01010101u, k4[0], k4[1]);
         both_halves(D, d[0][0], d[1][0]);
-        const u32x4 c = *reinterpret_cast<const u32x4*>(row + 16 + 32 * J + 16 * lh);
+    }
+    template <int J>
+    __device__ static void codes(const Raw& r, uint32_t, int b, int h, const uint32_t (&k4)[2], uint32_t (&q)[2]) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            q[0][i >> 1][i & 1] = less_pivot(c[i] & 0x0f0f0f0fu, k4[0]);
-            q[1][i >> 1][i & 1] = less_pivot((c[i] >> 4) & 0x0f0f0f0fu, k4[1]);
-        }
+        for (int i = 0; i < 2; ++i) q[i] = less_pivot((b ? r.c[2 * h + i] >> 4 : r.c[2 * h + i]) & 0x0f0f0f0fu, k4[b]);
     }
 };
 
@@ -231,33 +265,40 @@ template <> struct Unit<Q6KTile> {
     static constexpr int kSub = 2, kRow = 210, kCpr = 14, kPitch = 240;
     static constexpr bool kSums = false;
     __device__ static constexpr int at(int h, int lh) { return 16 * h + 8 * lh; }     // an MFMA is one scale's 16 weights
-    // 4 (c - 32) as signed bytes; d sc / 4 is exact
+    struct Raw {
+        uint32_t lo[2][2][3], hi[2][3], sc[2];     // [b][h], [h]
+        uint16_t d;
+    };
     template <int J>
-    __device__ static void step(const uint8_t* row, uint32_t sh, int lh, uint32_t (&q)[2][2][2], float (&d)[2][kSub],
-                                float&) {
+    __device__ static void read(const uint8_t* row, uint32_t sh, int lh, Raw& r) {
         const uint8_t* sb = row + sh;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            uint32_t hi[2];
-            lds_words<2>(sb + 128 + 32 * (J >> 1) + 16 * h + 8 * lh, sh, hi);
+            lds_span(sb + 128 + 32 * (J >> 1) + 16 * h + 8 * lh, sh, r.hi[h]);
 #pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                uint32_t lo[2];
-                lds_words<2>(sb + 64 * (J >> 1) + 32 * b + 16 * h + 8 * lh, sh, lo);
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const uint32_t l = J & 1 ? lo[i] >> 2 : lo[i] << 2;
-                    q[b][h][i] = (l & 0x3c3c3c3cu) | (((hi[i] ^ 0xaaaaaaaau) << (6 - 2 * (2 * (J & 1) + b))) & 0xc0c0c0c0u);
-                }
-            }
+            for (int b = 0; b < 2; ++b) lds_span(sb + 64 * (J >> 1) + 32 * b + 16 * h + 8 * lh, sh, r.lo[b][h]);
         }
-        uint32_t sc[1];
-        lds_words<1>(sb + 192 + 4 * J, sh, sc);
-        const float d4 = lds_half(sb + 208) * 0.25f;
+        lds_span(sb + 192 + 4 * J, sh, r.sc);
+        r.d = lds2(sb + 208);
+    }
+    // codes are 4 (c - 32); d sc / 4 is exact
+    template <int J>
+    __device__ static void scales(const Raw& r, uint32_t sh, int, float (&d)[2][kSub], float&, uint32_t (&)[2]) {
+        const uint32_t sc = word_of(r.sc, 0, sh);
+        const float d4 = half_bits_to_float(r.d) * 0.25f;
 #pragma unroll
         for (int b = 0; b < 2; ++b)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) d[b][h] = d4 * (float)(int8_t)(sc[0] >> (8 * (2 * b + h)));
+            for (int h = 0; h < 2; ++h) d[b][h] = d4 * (float)(int8_t)(sc >> (8 * (2 * b + h)));
+    }
+    template <int J>
+    __device__ static void codes(const Raw& r, uint32_t sh, int b, int h, const uint32_t (&)[2], uint32_t (&q)[2]) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const uint32_t lo = word_of(r.lo[b][h], i, sh);
+            const uint32_t hi = (word_of(r.hi[h], i, sh) ^ 0xaaaaaaaau) << (6 - 2 * (2 * (J & 1) + b));
+            q[i] = ((J & 1 ? lo >> 2 : lo << 2) & 0x3c3c3c3cu) | (hi & 0xc0c0c0c0u);
+        }
     }
 };
 
@@ -536,7 +577,7 @@ struct TileShape {
     static constexpr int kCHS = TN > 32 || kP > 1 || KG > 1 ? 1 : 2;
     // waves of a SIMD that the registers are cut for; few tokens leave the
     // decoding as the bound, and it takes four waves to keep that going
-    static constexpr int kOcc = TN > 32 || kP > 1 ? 2 : 3;
+    static constexpr int kOcc = TN > 32 || kP > 1 || Unit<F>::kSub > 1 ? 2 : 3;
     static constexpr int kCH = kCHS * KG;
     static constexpr int kXL = TN * 8 * kCH / kTileThreads;         // 8-column pieces of x per thread and chunk
     static constexpr int kPitch = 128 * kCH + 16;                   // bytes of a staged token: an odd number of 16-byte units, so 8 tokens hit distinct banks
@@ -699,18 +740,29 @@ __global__ __launch_bounds__(kTileThreads, (TileShape<F, XT, TN, KG>::kOcc)) voi
         }
 #pragma unroll
         for (int i = 0; i < S::kXL; ++i) {
-            const int tok = xt + kXStep * i;
             u32x4 p[S::kP];
             g.x[i].pieces(p);
 #pragma unroll
             for (int k = 0; k < S::kP; ++k)
-                *reinterpret_cast<u32x4*>(buf + (k * TN + tok) * S::kPitch + 16 * xc) = p[k];
-            if constexpr (U::kSums) {
-                float t = g.x[i].sum();      // of 8 columns; four lanes hold a block's 32
-                t += dpp_mov<0xB1>(t);
-                t += dpp_mov<0x4E>(t);
-                if ((xc & 3) == 0)
-                    *reinterpret_cast<u32x4*>(buf + S::kX + ((xc >> 2) * TN + tok) * 16) = min_operand<1>(t);
+                *reinterpret_cast<u32x4*>(buf + (k * TN + xt + kXStep * i) * S::kPitch + 16 * xc) = p[k];
+        }
+        if constexpr (U::kSums) {
+            // a block's sum is over four neighbouring lanes (eight columns
+            // each) and then in all four; the k-th of them writes the k-th
+            // of up to four tokens' sums
+#pragma unroll
+            for (int i0 = 0; i0 < S::kXL; i0 += 4) {
+                float own = 0.f;
+#pragma unroll
+                for (int k = 0; k < 4 && i0 + k < S::kXL; ++k) {
+                    float t = g.x[i0 + k].sum();
+                    t += dpp_mov<0xB1>(t);
+                    t += dpp_mov<0x4E>(t);
+                    own = (xc & 3) == k ? t : own;
+                }
+                if ((xc & 3) + i0 < S::kXL)
+                    *reinterpret_cast<u32x4*>(buf + S::kX + ((xc >> 2) * TN + xt + kXStep * (i0 + (xc & 3))) * 16) =
+                        min_operand<1>(own);
             }
         }
     };
@@ -721,39 +773,56 @@ __global__ __launch_bounds__(kTileThreads, (TileShape<F, XT, TN, KG>::kOcc)) voi
 #pragma unroll
         for (int i = 0; i < 16; ++i) acc[t][i] = 0.f;
 
-    // Step J of round s, the sc0-th of those staged in buf: decode, then for
-    // each block and 32 tokens (a piece) its MFMAs, between the scalings of
-    // the piece before it: a piece's results are 16 fused multiply-adds a
-    // lane, about as long as its two MFMAs, so the two pipes run side by side
-    // with two pieces' results live.
-    auto compute = [&](auto jc, int s, int sc0, const uint8_t* buf) __attribute__((always_inline)) {
-        constexpr int J = decltype(jc)::value;
-        const int blk = 8 * (KG * s + wk) + 2 * J;
-        uint32_t q[2][2][2];
+    // A step's operands: codes by block and MFMA, scales, mu.
+    struct Ops {
         u32x4 op[2][2];
-        float mu = 0.f, d[2][U::kSub];
-        U::template step<J>(slot_row, (wown + sup_of(s) * U::kRow) & 2, lh, q, d, mu);
-#pragma unroll
-        for (int b = 0; b < 2; ++b)
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-                op[b][h] = u32x4{XOp<XT>::pair(sbyte(q[b][h][0], 0), sbyte(q[b][h][0], 1)),
-                                 XOp<XT>::pair(sbyte(q[b][h][0], 2), sbyte(q[b][h][0], 3)),
-                                 XOp<XT>::pair(sbyte(q[b][h][1], 0), sbyte(q[b][h][1], 1)),
-                                 XOp<XT>::pair(sbyte(q[b][h][1], 2), sbyte(q[b][h][1], 3))};
+        float d[2][U::kSub], mu;
+    };
+    typename U::Raw raw;
+    Ops ops[2];
+    uint32_t k4[2];
+    auto row_sh = [&](int s) __attribute__((always_inline)) { return (wown + sup_of(s) * U::kRow) & 2; };
+    auto read_raw = [&](auto jc, int s) __attribute__((always_inline)) {
+        U::template read<decltype(jc)::value>(slot_row, row_sh(s), lh, raw);
+    };
+    auto decode_scales = [&](auto jc, int s, Ops& o) __attribute__((always_inline)) {
+        constexpr int J = decltype(jc)::value;
+        o.mu = 0.f;
+        U::template scales<J>(raw, row_sh(s), lh, o.d, o.mu, k4);
         // past the row the scales are 0 (and so are the activations); the
         // asm keeps this a branch, which only a row's last round takes
         if (8 * (KG * s + wk) + 8 > a.nb) {
             asm volatile("");
+            const int blk = 8 * (KG * s + wk) + 2 * J;
 #pragma unroll
             for (int b = 0; b < 2; ++b)
                 if (blk + b >= a.nb) {
 #pragma unroll
-                    for (int h = 0; h < U::kSub; ++h) d[b][h] = 0.f;
+                    for (int h = 0; h < U::kSub; ++h) o.d[b][h] = 0.f;
                 }
-            if (blk + lh >= a.nb) mu = 0.f;
+            if (blk + lh >= a.nb) o.mu = 0.f;
         }
+    };
+    auto decode_codes = [&](auto jc, int s, auto pc, Ops& o) __attribute__((always_inline)) {
+        constexpr int b = decltype(pc)::value >> 1, h = decltype(pc)::value & 1;
+        uint32_t q[2];
+        U::template codes<decltype(jc)::value>(raw, row_sh(s), b, h, k4, q);
+        o.op[b][h] = u32x4{XOp<XT>::pair(sbyte(q[0], 0), sbyte(q[0], 1)), XOp<XT>::pair(sbyte(q[0], 2), sbyte(q[0], 3)),
+                           XOp<XT>::pair(sbyte(q[1], 0), sbyte(q[1], 1)), XOp<XT>::pair(sbyte(q[1], 2), sbyte(q[1], 3))};
+        asm volatile("" : "+v"(o.op[b][h]));      // here, not where the next step uses it
+    };
 
+    // Step J of round s, the sc0-th of those staged in buf.  For each block
+    // and 32 tokens (a piece) its MFMAs, between the scalings of the piece
+    // before it (16 fused multiply-adds a lane, about as long as the two
+    // MFMAs) and the decoding of the next step (round sn) in four parts: the
+    // matrix and the vector pipe run side by side, with two pieces' results
+    // live.
+    auto compute = [&](auto jc, int sn, int sc0, const uint8_t* buf) __attribute__((always_inline)) {
+        constexpr int J = decltype(jc)::value;
+        const std::integral_constant<int, (J + 1) & 3> jn;
+        const Ops& cur = ops[J & 1];
+        Ops& next = ops[(J + 1) & 1];
         const uint8_t* xq0 = buf + lr * S::kPitch + 128 * sc0 + 2 * U::at(0, 1) * lh;
         constexpr int kPieces = 2 * S::kTS;
         constexpr int kMf = 2 * S::kP;                        // MFMAs of a piece
@@ -769,6 +838,13 @@ __global__ __launch_bounds__(kTileThreads, (TileShape<F, XT, TN, KG>::kOcc)) voi
                         *reinterpret_cast<const u32x4*>(xq0 + (k * TN + 32 * t) * S::kPitch + 64 * b + 2 * U::at(h, 0));
         };
         read_x(std::integral_constant<int, 0>{});
+        decode_scales(jn, sn, next);
+        decode_codes(jn, sn, std::integral_constant<int, 0>{}, next);
+        constexpr int kSlots = (kPieces + 1) * kMf;
+        // the wave that multiplies goes before those that stage and decode
+        // (2048 tokens x 14336 x 4096 Q4_0 397 -> 386 us, weights for single
+        // tokens 137 -> 127)
+        __builtin_amdgcn_s_setprio(1);
         static_for(std::make_integer_sequence<int, kPieces + 1>{}, [&](auto nc) __attribute__((always_inline)) {
             constexpr int e = decltype(nc)::value;
             constexpr int b = e / S::kTS;
@@ -786,23 +862,29 @@ __global__ __launch_bounds__(kTileThreads, (TileShape<F, XT, TN, KG>::kOcc)) voi
                     } else {
                         c = dot[e & 1][o];
                     }
-                    dot[e & 1][o] = XOp<XT>::mfma(xq[e & 1][k][h], op[b][h], c);
+                    dot[e & 1][o] = XOp<XT>::mfma(xq[e & 1][k][h], cur.op[b][h], c);
                 }
                 if constexpr (e > 0) {
                     // the m-th share of the piece before
                     constexpr int all = 16 * U::kSub, i0 = all * m / kMf, i1 = all * (m + 1) / kMf;
 #pragma unroll
                     for (int i = i0; i < i1; ++i)
-                        acc[pt][i & 15] = __builtin_fmaf(d[pb][i >> 4], dot[pe & 1][i >> 4][i & 15], acc[pt][i & 15]);
+                        acc[pt][i & 15] = __builtin_fmaf(cur.d[pb][i >> 4], dot[pe & 1][i >> 4][i & 15], acc[pt][i & 15]);
                 }
+                static_for(std::make_integer_sequence<int, 3>{}, [&](auto tc) __attribute__((always_inline)) {
+                    constexpr int t = decltype(tc)::value + 1;
+                    if constexpr (e * kMf + m == kSlots * t / 4 - 1)
+                        decode_codes(jn, sn, std::integral_constant<int, t>{}, next);
+                });
                 __builtin_amdgcn_sched_barrier(0x4 | 0x10);            // scalar and global memory may pass
             });
             // the scalings stay here (they are used a step later only)
             if constexpr (e > 0) asm volatile("" : "+v"(acc[pt]));
         });
+        __builtin_amdgcn_s_setprio(0);
         if constexpr (U::kSums) {
             // mu times the block sums of x, both blocks of the step in one MFMA
-            const u32x4 mw = min_operand<0>(mu);
+            const u32x4 mw = min_operand<0>(cur.mu);
             const u32x4* mx = reinterpret_cast<const u32x4*>(buf + S::kX) + (2 * sc0 + lh) * TN + lr;
 #pragma unroll
             for (int t = 0; t < S::kTS; ++t) acc[t] = XOp<__bf16>::mfma(mx[32 * t], mw, acc[t]);
@@ -816,17 +898,29 @@ __global__ __launch_bounds__(kTileThreads, (TileShape<F, XT, TN, KG>::kOcc)) voi
 #pragma unroll
         for (int i = 0; i < S::kXL; ++i) gx.x[i].zero();       // tokens past the tile's stay 0
         load_x(0, gx);
+        put_w();
+        load_w(1);
+        const std::integral_constant<int, 0> j0;
+        read_raw(j0, 0);
+        decode_scales(j0, 0, ops[0]);
+        static_for(std::make_integer_sequence<int, 4>{},
+                   [&](auto pc) __attribute__((always_inline)) { decode_codes(j0, 0, pc, ops[0]); });
+        read_raw(std::integral_constant<int, 1>{}, 0);
         put_x(0, gx);
         load_x(1, gx);
         __syncthreads();
         for (int s = 0; s < rounds; ++s) {
-            // the slot's last reads are this wave's own: LDS keeps their order
-            put_w();
-            load_w(s + 1);
             static_for(std::make_integer_sequence<int, 4>{}, [&](auto jc) __attribute__((always_inline)) {
                 constexpr int j = decltype(jc)::value;
                 const int c = kParts * s + j / S::kCHS;
-                compute(jc, s, S::kCHS * wk + j % S::kCHS, lds + (c & 1) * S::kBuf);
+                compute(jc, j == 3 ? s + 1 : s, S::kCHS * wk + j % S::kCHS, lds + (c & 1) * S::kBuf);
+                // the words of the step after next; the slot changes once its
+                // last step's are read (LDS keeps a wave's order)
+                if constexpr (j == 2) {
+                    put_w();
+                    load_w(s + 2);
+                }
+                read_raw(std::integral_constant<int, (j + 2) & 3>{}, j >= 2 ? s + 1 : s);
                 if constexpr (j % S::kCHS == S::kCHS - 1) {
                     put_x(c + 1, gx);                // past the last chunk: not read
                     load_x(c + 2, gx);
