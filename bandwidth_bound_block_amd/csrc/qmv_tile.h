@@ -385,7 +385,7 @@ __device__ __forceinline__ u32x4 min_operand(float v) {
 struct TileDev {
     const uint8_t* W;
     int64_t estride;
-    int rows, nb, row_tiles;
+    int rows, nb, row_tiles, row_unit;
     const int32_t* plan;
     int n_items, n_groups, top_k, plan_tile;
     const void* x;
@@ -441,46 +441,55 @@ constexpr int kLoraPitch = 2 * kLoraRanks + 16;      // bytes of a token's piece
 // tokens that hold one of its own, and the sums taken over for those tokens
 // alone.  v and B are split into three bf16 pieces each (bf16 B has one); the
 // products left out are 2^-24 of the sum.  v is staged in `lds` by the whole
-// workgroup; waves with add false only stage.
-template <int TN>
+// workgroup; of the KG waves that share the rows, wave wk takes every KG-th
+// adapter (their sums meet in the epilogue).  An adapter's rows are loaded
+// while those of the one before are multiplied: 40 requests of 101 tokens
+// would else wait for 25 loads a tile, one after the other.
+template <int TN, int KG>
 __device__ __forceinline__ void add_adapters(const LoraTile& l, const int* s_adapter, int first, int count, int n_items,
-                                             int rows, int row, bool add, uint8_t* lds, f32x16 (&acc)[TN / 32]) {
+                                             int rows, int row, int wk, uint8_t* lds, f32x16 (&acc)[TN / 32]) {
+    constexpr int kSteps = kLoraRanks / 16;
     const int tid = threadIdx.x, lane = tid & 63, lr = lane & 31, lh = lane >> 5;
     for (int c0 = 0; c0 < l.rank; c0 += kLoraRanks) {
         const int ranks = min(kLoraRanks, l.rank - c0);
         const int steps = (ranks + 15) >> 4;
         __syncthreads();
-        // fours of ranks, zeros past the last up to whole steps
-        for (int i = tid; i < TN * 4 * steps; i += kTileThreads) {
-            const int j = i / (4 * steps), r = 4 * (i % (4 * steps));
-            f32x4 x = {0.f, 0.f, 0.f, 0.f};
-            if (j < count) {
+        // fours of ranks, zeros past the last up to whole steps; all loads first
+        constexpr int kQuads = TN * 4 * kSteps / kTileThreads;
+        f32x4 x[kQuads];
+#pragma unroll
+        for (int q = 0; q < kQuads; ++q) {
+            const int i = tid + q * kTileThreads, j = i / (4 * kSteps), r = 4 * (i % (4 * kSteps));
+            x[q] = f32x4{0.f, 0.f, 0.f, 0.f};
+            if (j < count && r < ranks) {
                 const float* v = l.v + (int64_t)(first + j) * l.rank + c0 + r;
-                if (l.rank % 4 == 0) {
-                    if (r < ranks)
-                        for (int p = 0; p < l.parts; ++p)
-                            x += *reinterpret_cast<const f32x4*>(v + (int64_t)p * n_items * l.rank);
-                } else {
-                    for (int p = 0; p < l.parts; ++p)
+                for (int p = 0; p < l.parts; ++p, v += (int64_t)n_items * l.rank) {
+                    if (l.rank % 4 == 0) {
+                        x[q] += *reinterpret_cast<const f32x4*>(v);
+                    } else {
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
-                            if (r + k < ranks) x[k] += v[(int64_t)p * n_items * l.rank + k];
+                            if (r + k < ranks) x[q][k] += v[k];
+                    }
                 }
             }
+        }
+#pragma unroll
+        for (int q = 0; q < kQuads; ++q) {
+            const int i = tid + q * kTileThreads, j = i / (4 * kSteps), r = 4 * (i % (4 * kSteps));
 #pragma unroll
             for (int k = 0; k < 3; ++k) {
                 uint32_t w[2];
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    w[e] = __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{x[2 * e], x[2 * e + 1]}, bf16x2));
-                    x[2 * e] -= __builtin_bit_cast(float, w[e] << 16);
-                    x[2 * e + 1] -= __builtin_bit_cast(float, w[e] & 0xffff0000u);
+                    w[e] = __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{x[q][2 * e], x[q][2 * e + 1]}, bf16x2));
+                    x[q][2 * e] -= __builtin_bit_cast(float, w[e] << 16);
+                    x[q][2 * e + 1] -= __builtin_bit_cast(float, w[e] & 0xffff0000u);
                 }
                 *reinterpret_cast<uint2*>(lds + (k * TN + j) * kLoraPitch + 2 * r) = uint2{w[0], w[1]};
             }
         }
         __syncthreads();
-        if (!add) continue;
         uint32_t todo[TN / 32];
         int id[TN / 32];
 #pragma unroll
@@ -488,46 +497,63 @@ __device__ __forceinline__ void add_adapters(const LoraTile& l, const int* s_ada
             id[t] = s_adapter[32 * t + lr];
             todo[t] = (uint32_t)__ballot(32 * t + lr < count && (unsigned)id[t] < (unsigned)l.n_adapters);
         }
-        while (true) {
-            int ad = -1;
+        // the next adapter of this wave's turn (-1: none), its tokens
+        int turn = 0;
+        auto next_adapter = [&](uint32_t (&own)[TN / 32]) __attribute__((always_inline)) {
+            while (true) {
+                int ad = -1;
 #pragma unroll
-            for (int t = 0; t < TN / 32; ++t)
-                if (ad < 0 && todo[t]) ad = __builtin_amdgcn_readlane(id[t], __builtin_ctz(todo[t]));
-            if (ad < 0) break;
-            const int64_t brow = ((int64_t)ad * rows + row) * l.rank + c0;
-            uint32_t own[TN / 32];
+                for (int t = 0; t < TN / 32; ++t)
+                    if (ad < 0 && todo[t]) ad = __builtin_amdgcn_readlane(id[t], __builtin_ctz(todo[t]));
 #pragma unroll
-            for (int t = 0; t < TN / 32; ++t) {
-                own[t] = (uint32_t)__ballot(id[t] == ad) & todo[t];
-                todo[t] &= ~own[t];
+                for (int t = 0; t < TN / 32; ++t) {
+                    own[t] = (uint32_t)__ballot(id[t] == ad) & todo[t];
+                    todo[t] &= ~own[t];
+                }
+                if (ad < 0 || turn++ % KG == wk) return ad;
             }
-            u32x4 bp[kLoraRanks / 16][3];
+        };
+        const bool b16 = l.b_type != QMV_X_F32 && l.vec;      // rows of B in 16-byte pieces of eight ranks
+        auto load_b = [&](int ad, u32x4 (&w)[kSteps]) __attribute__((always_inline)) {
+            if (!b16 || ad < 0) return;
+            const uint16_t* b = static_cast<const uint16_t*>(l.B) + ((int64_t)ad * rows + row) * l.rank + c0;
 #pragma unroll
-            for (int s = 0; s < kLoraRanks / 16; ++s) {
-                if (s >= steps) continue;
+            for (int s = 0; s < kSteps; ++s) {
                 const int r0 = 16 * s + 8 * lh;
-                X8<float> b;
-                if (l.vec && r0 + 8 <= ranks) {
-                    if (l.b_type == QMV_X_F32) {
-                        b.load(static_cast<const float*>(l.B) + brow + r0, true);
-                    } else {
-                        const u32x4 w = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(l.B) + brow + r0);
+                w[s] = u32x4{0, 0, 0, 0};
+                if (r0 < ranks) w[s] = *reinterpret_cast<const u32x4*>(b + r0);
+            }
+        };
+        uint32_t own[TN / 32], own2[TN / 32];
+        u32x4 w[kSteps], w2[kSteps];
+        int ad = next_adapter(own);
+        load_b(ad, w);
+        while (ad >= 0) {
+            const int ad2 = next_adapter(own2);
+            load_b(ad2, w2);
+            const int64_t brow = ((int64_t)ad * rows + row) * l.rank + c0;
+            u32x4 bp[kSteps][3];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const bool half = l.b_type == QMV_X_F16;
-                            b.v[2 * i] = half ? half_bits_to_float(w[i]) : __builtin_bit_cast(float, w[i] << 16);
-                            b.v[2 * i + 1] =
-                                half ? half_bits_to_float(w[i] >> 16) : __builtin_bit_cast(float, w[i] & 0xffff0000u);
-                        }
+            for (int s = 0; s < kSteps; ++s) {
+                if (s >= steps) continue;
+                X8<float> b;
+                if (b16) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const bool half = l.b_type == QMV_X_F16;
+                        b.v[2 * i] = half ? half_bits_to_float(w[s][i]) : __builtin_bit_cast(float, w[s][i] << 16);
+                        b.v[2 * i + 1] = half ? half_bits_to_float(w[s][i] >> 16)
+                                              : __builtin_bit_cast(float, w[s][i] & 0xffff0000u);
                     }
                 } else {
+                    const int r0 = 16 * s + 8 * lh;
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
                         const int64_t at = brow + min(r0 + i, ranks - 1);
-                        const float w = l.b_type == QMV_X_F32   ? static_cast<const float*>(l.B)[at]
+                        const float f = l.b_type == QMV_X_F32   ? static_cast<const float*>(l.B)[at]
                                         : l.b_type == QMV_X_F16 ? (float)static_cast<const _Float16*>(l.B)[at]
                                                                 : (float)static_cast<const __bf16*>(l.B)[at];
-                        b.v[i] = r0 + i < ranks ? w : 0.f;
+                        b.v[i] = r0 + i < ranks ? f : 0.f;
                     }
                 }
                 b.pieces(bp[s]);
@@ -539,7 +565,7 @@ __device__ __forceinline__ void add_adapters(const LoraTile& l, const int* s_ada
 #pragma unroll
                 for (int i = 0; i < 16; ++i) sum[i] = 0.f;
 #pragma unroll
-                for (int s = 0; s < kLoraRanks / 16; ++s) {
+                for (int s = 0; s < kSteps; ++s) {
                     if (s >= steps) continue;
 #pragma unroll
                     for (int k = 2; k >= 0; --k) {
@@ -556,12 +582,18 @@ __device__ __forceinline__ void add_adapters(const LoraTile& l, const int* s_ada
                 for (int i = 0; i < 16; ++i)
                     if (mine >> (8 * (i >> 2) + (i & 3)) & 1) acc[t][i] += sum[i];
             }
+            ad = ad2;
+#pragma unroll
+            for (int t = 0; t < TN / 32; ++t) own[t] = own2[t];
+#pragma unroll
+            for (int s = 0; s < kSteps; ++s) w[s] = w2[s];
         }
     }
 }
 
 constexpr int kXcds = 8;          // workgroups go to the XCDs in turn
 constexpr int kTokGroup = 8;      // token tiles that an XCD takes together
+constexpr int kRowGroup = 32;     // compute units of an XCD: most row tiles of a unit
 // A wave takes 32 weight rows by TN tokens.  Its step is two blocks of each
 // row, decoded by the lanes that multiply them, so no wave waits for
 // another's weights.  KG waves of a workgroup share 32 rows and take their
@@ -577,8 +609,14 @@ struct TileShape {
     static constexpr int kCHS = TN > 32 || kP > 1 || KG > 1 ? 1 : 2;
     // waves of a SIMD that the registers are cut for; few tokens leave the
     // decoding as the bound, and it takes four waves to keep that going
-    static constexpr int kOcc = TN > 32 || kP > 1 || Unit<F>::kSub > 1 ? 2 : 3;
+    static constexpr int kOcc = TN > 32 || kP > 1 ? 2 : 3;
+    // whether a step is decoded during the one before it; for few tokens
+    // Q6_K's words and a second set of operands would take the third wave
+    // (64 tokens through 128 experts 180 us against 200)
+    static constexpr bool kAhead = TN > 32 || Unit<F>::kSub == 1;
     static constexpr int kCH = kCHS * KG;
+    // chunks of activations on their way besides the one being staged
+    static constexpr int kXAhead = TN < 128 && kP == 1 && Unit<F>::kCpr <= 10 ? 2 : 1;      // as registers allow
     static constexpr int kXL = TN * 8 * kCH / kTileThreads;         // 8-column pieces of x per thread and chunk
     static constexpr int kPitch = 128 * kCH + 16;                   // bytes of a staged token: an odd number of 16-byte units, so 8 tokens hit distinct banks
     static constexpr int kX = kP * TN * kPitch;
@@ -604,7 +642,7 @@ __global__ __launch_bounds__(kTileThreads, (TileShape<F, XT, TN, KG>::kOcc)) voi
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
 
-    const int split = a.plan_tile / TN;      // workgroups along a plan's tile
+    const int split = a.plan_tile / TN;      // workgroups along a plan's tile (1 without a plan)
     int tok_tiles;
     if (a.plan) {
         // a plan of other items or groups than the call's is not followed
@@ -614,17 +652,33 @@ __global__ __launch_bounds__(kTileThreads, (TileShape<F, XT, TN, KG>::kOcc)) voi
     } else {
         tok_tiles = (a.n_items + TN - 1) / TN;
     }
-    const int total = tok_tiles * a.row_tiles;
-    if ((int)blockIdx.x >= total) return;
-    // Tiles in runs, one run to an XCD, and within it kTokGroup token tiles
-    // side by side down the rows: the tiles an XCD works on at one time
-    // share their weights and activations in its L2.
-    const int xcd = blockIdx.x % kXcds;
-    const int id = xcd * (total / kXcds) + min(xcd, total % kXcds) + blockIdx.x / kXcds;
-    const int t0 = id / (kTokGroup * a.row_tiles) * kTokGroup;
-    const int tw = min(kTokGroup, tok_tiles - t0);
-    const int in = id - t0 * a.row_tiles;
-    const int rt = in / tw, tt = t0 + in % tw;
+    const int xcd = blockIdx.x % kXcds, turn = blockIdx.x / kXcds;
+    int rt, tt;
+    if (split == 1) {
+        // Tiles in runs, one run to an XCD, and within it kTokGroup token
+        // tiles side by side down the rows: the tiles an XCD works on at one
+        // time share their weights and activations in its L2.
+        const int total = tok_tiles * a.row_tiles;
+        if ((int)blockIdx.x >= total) return;
+        const int id = xcd * (total / kXcds) + min(xcd, total % kXcds) + turn;
+        const int t0 = id / (kTokGroup * a.row_tiles) * kTokGroup;
+        const int tw = min(kTokGroup, tok_tiles - t0);
+        const int in = id - t0 * a.row_tiles;
+        rt = in / tw;
+        tt = t0 + in % tw;
+    } else {
+        // A plan's tile that is split has parts past its items, which are
+        // empty.  Units of all parts of a tile by row_unit row tiles go to
+        // the XCDs in turn, so that these are as busy as each other, and
+        // within a unit a part's rows follow each other (side by side, the
+        // busy workgroups all came to every fourth compute unit: 66 us
+        // against 21).
+        const int size = split * a.row_unit, units = (a.row_tiles + a.row_unit - 1) / a.row_unit;
+        const int unit = turn / size * kXcds + xcd, at = turn % size;
+        rt = unit % units * a.row_unit + at % a.row_unit;
+        tt = unit / units * split + at / a.row_unit;
+        if (tt >= tok_tiles || rt >= a.row_tiles) return;
+    }
 
     const int out_rows = a.swiglu ? S::kTM / 2 : S::kTM;
     const int row0 = rt * out_rows;
@@ -821,8 +875,8 @@ __global__ __launch_bounds__(kTileThreads, (TileShape<F, XT, TN, KG>::kOcc)) voi
     auto compute = [&](auto jc, int sn, int sc0, const uint8_t* buf) __attribute__((always_inline)) {
         constexpr int J = decltype(jc)::value;
         const std::integral_constant<int, (J + 1) & 3> jn;
-        const Ops& cur = ops[J & 1];
-        Ops& next = ops[(J + 1) & 1];
+        const Ops& cur = ops[S::kAhead ? J & 1 : 0];
+        Ops& next = ops[S::kAhead ? (J + 1) & 1 : 0];
         const uint8_t* xq0 = buf + lr * S::kPitch + 128 * sc0 + 2 * U::at(0, 1) * lh;
         constexpr int kPieces = 2 * S::kTS;
         constexpr int kMf = 2 * S::kP;                        // MFMAs of a piece
@@ -838,8 +892,10 @@ __global__ __launch_bounds__(kTileThreads, (TileShape<F, XT, TN, KG>::kOcc)) voi
                         *reinterpret_cast<const u32x4*>(xq0 + (k * TN + 32 * t) * S::kPitch + 64 * b + 2 * U::at(h, 0));
         };
         read_x(std::integral_constant<int, 0>{});
-        decode_scales(jn, sn, next);
-        decode_codes(jn, sn, std::integral_constant<int, 0>{}, next);
+        if constexpr (S::kAhead) {
+            decode_scales(jn, sn, next);
+            decode_codes(jn, sn, std::integral_constant<int, 0>{}, next);
+        }
         constexpr int kSlots = (kPieces + 1) * kMf;
         // the wave that multiplies goes before those that stage and decode
         // (2048 tokens x 14336 x 4096 Q4_0 397 -> 386 us, weights for single
@@ -873,7 +929,7 @@ __global__ __launch_bounds__(kTileThreads, (TileShape<F, XT, TN, KG>::kOcc)) voi
                 }
                 static_for(std::make_integer_sequence<int, 3>{}, [&](auto tc) __attribute__((always_inline)) {
                     constexpr int t = decltype(tc)::value + 1;
-                    if constexpr (e * kMf + m == kSlots * t / 4 - 1)
+                    if constexpr (S::kAhead && e * kMf + m == kSlots * t / 4 - 1)
                         decode_codes(jn, sn, std::integral_constant<int, t>{}, next);
                 });
                 __builtin_amdgcn_sched_barrier(0x4 | 0x10);            // scalar and global memory may pass
@@ -894,44 +950,65 @@ __global__ __launch_bounds__(kTileThreads, (TileShape<F, XT, TN, KG>::kOcc)) voi
     // One barrier a chunk: the buffer of chunk c + 1 was last read in chunk
     // c - 1, before the barrier that ended it.
     {
-        XRegs gx;
+        XRegs gx[S::kXAhead];                  // chunk c in gx[c % kXAhead]
 #pragma unroll
-        for (int i = 0; i < S::kXL; ++i) gx.x[i].zero();       // tokens past the tile's stay 0
-        load_x(0, gx);
-        put_w();
-        load_w(1);
-        const std::integral_constant<int, 0> j0;
-        read_raw(j0, 0);
-        decode_scales(j0, 0, ops[0]);
-        static_for(std::make_integer_sequence<int, 4>{},
-                   [&](auto pc) __attribute__((always_inline)) { decode_codes(j0, 0, pc, ops[0]); });
-        read_raw(std::integral_constant<int, 1>{}, 0);
-        put_x(0, gx);
-        load_x(1, gx);
+        for (int k = 0; k < S::kXAhead; ++k)
+#pragma unroll
+            for (int i = 0; i < S::kXL; ++i) gx[k].x[i].zero();       // tokens past the tile's stay 0
+        load_x(0, gx[0]);
+        if constexpr (S::kXAhead > 1) load_x(1, gx[1]);
+        auto decode = [&](auto jc, int s, Ops& o) __attribute__((always_inline)) {
+            decode_scales(jc, s, o);
+            static_for(std::make_integer_sequence<int, 4>{},
+                       [&](auto pc) __attribute__((always_inline)) { decode_codes(jc, s, pc, o); });
+        };
+        if constexpr (S::kAhead) {
+            const std::integral_constant<int, 0> j0;
+            put_w();
+            load_w(1);
+            read_raw(j0, 0);
+            decode(j0, 0, ops[0]);
+            read_raw(std::integral_constant<int, 1>{}, 0);
+        }
+        put_x(0, gx[0]);
+        load_x(S::kXAhead, gx[0]);
         __syncthreads();
         for (int s = 0; s < rounds; ++s) {
             static_for(std::make_integer_sequence<int, 4>{}, [&](auto jc) __attribute__((always_inline)) {
                 constexpr int j = decltype(jc)::value;
                 const int c = kParts * s + j / S::kCHS;
-                compute(jc, j == 3 ? s + 1 : s, S::kCHS * wk + j % S::kCHS, lds + (c & 1) * S::kBuf);
-                // the words of the step after next; the slot changes once its
-                // last step's are read (LDS keeps a wave's order)
-                if constexpr (j == 2) {
-                    put_w();
-                    load_w(s + 2);
+                // the slot changes once its last step's words are read (LDS
+                // keeps a wave's order)
+                if constexpr (!S::kAhead) {
+                    if constexpr (j == 0) {
+                        put_w();
+                        load_w(s + 1);
+                    }
+                    read_raw(jc, s);
+                    decode(jc, s, ops[0]);
                 }
-                read_raw(std::integral_constant<int, (j + 2) & 3>{}, j >= 2 ? s + 1 : s);
+                compute(jc, j == 3 ? s + 1 : s, S::kCHS * wk + j % S::kCHS, lds + (c & 1) * S::kBuf);
+                if constexpr (S::kAhead) {
+                    // the words of the step after next
+                    if constexpr (j == 2) {
+                        put_w();
+                        load_w(s + 2);
+                    }
+                    read_raw(std::integral_constant<int, (j + 2) & 3>{}, j >= 2 ? s + 1 : s);
+                }
                 if constexpr (j % S::kCHS == S::kCHS - 1) {
-                    put_x(c + 1, gx);                // past the last chunk: not read
-                    load_x(c + 2, gx);
+                    // past the last chunk: not read
+                    XRegs& g = gx[(j / S::kCHS + 1) % S::kXAhead];
+                    put_x(c + 1, g);
+                    load_x(c + 1 + S::kXAhead, g);
                     __syncthreads();
                 }
             });
         }
     }
     if constexpr (LORA)
-        add_adapters<TN>(a.lora, s_adapter, start, count, a.n_items, a.rows, min(row0 + wr + lr, a.rows - 1), wk == 0,
-                         lds, acc);
+        add_adapters<TN, KG>(a.lora, s_adapter, start, count, a.n_items, a.rows, min(row0 + wr + lr, a.rows - 1), wk, lds,
+                             acc);
     __syncthreads();
 
     // results through LDS, so that stores run along the rows
@@ -968,6 +1045,7 @@ __global__ __launch_bounds__(kTileThreads, (TileShape<F, XT, TN, KG>::kOcc)) voi
 template <class F, class XT, int TN, int KG, bool LORA>
 int32_t launch_tile(const TileCall& c, int plan_tile, hipStream_t st) {
     using S = TileShape<F, XT, TN, KG>;
+    if (!c.plan) plan_tile = TN;
     const int out_rows = c.swiglu ? S::kTM / 2 : S::kTM;
     TileDev d;
     d.W = c.W;
@@ -979,7 +1057,7 @@ int32_t launch_tile(const TileCall& c, int plan_tile, hipStream_t st) {
     d.n_items = (int)c.n_items;
     d.n_groups = c.n_groups;
     d.top_k = c.top_k;
-    d.plan_tile = plan_tile;
+    d.plan_tile = plan_tile;      // without a plan, TN
     d.x = c.x;
     d.xs_tok = c.xs_tok;
     d.xs_slot = c.xs_slot;
@@ -993,16 +1071,22 @@ int32_t launch_tile(const TileCall& c, int plan_tile, hipStream_t st) {
     d.tiles_at = (int)plan_tiles_at(c.n_groups);
     d.order_at = c.plan ? (int)plan_order_at(c.n_items, c.n_groups) : 0;
     d.lora = c.lora;
-    const int64_t tiles = c.plan ? plan_tile_bound(c.n_items, c.n_groups, plan_tile) * (plan_tile / TN)
-                                 : (c.n_items + TN - 1) / TN;
-    if (tiles * d.row_tiles > 0x7fffffff)
-        return fail(QMV_EINVAL, "qmv: %lld tiles exceed a launch", (long long)(tiles * d.row_tiles));
+    const int units = (d.row_tiles + kRowGroup - 1) / kRowGroup;
+    d.row_unit = (d.row_tiles + units - 1) / units;
+    const int split = plan_tile / TN;
+    const int64_t whole = c.plan ? plan_tile_bound(c.n_items, c.n_groups, plan_tile) : (c.n_items + plan_tile - 1) / plan_tile;
+    int64_t grid;
+    if (split == 1)
+        grid = whole * d.row_tiles;
+    else
+        grid = (whole * units + kXcds - 1) / kXcds * kXcds * split * d.row_unit;
+    if (grid > 0x7fffffff) return fail(QMV_EINVAL, "qmv: %lld tiles exceed a launch", (long long)grid);
     auto kern = tile_kernel<F, XT, TN, KG, LORA>;
     size_t dyn_max = 0;
     if (const int32_t e = lds_limit(reinterpret_cast<const void*>(kern), kLdsMax, "qmv", &dyn_max)) return e;
     const size_t lds = std::max<size_t>(S::kLds, LORA ? S::kLora : 0);
     if (lds > dyn_max) return fail(QMV_EHIP, "qmv: the tile kernel's LDS exceeds the device's");
-    hipLaunchKernelGGL(kern, dim3((unsigned)(tiles * d.row_tiles)), dim3(kTileThreads), lds, st, d);
+    hipLaunchKernelGGL(kern, dim3((unsigned)grid), dim3(kTileThreads), lds, st, d);
     return check_launch("qmv");
 }
 
@@ -1011,23 +1095,34 @@ int32_t launch_tile_s(const TileCall& c, int tile, hipStream_t st) {
     return c.lora.rank ? launch_tile<F, XT, TN, KG, true>(c, tile, st) : launch_tile<F, XT, TN, KG, false>(c, tile, st);
 }
 
-// fp32 activations take three times the LDS and MFMAs: 64 tokens by 256 rows
-// where 16-bit ones take 128 by 128.
+// Which tile.  TN 128 by 128 rows (fp32 activations, of three times the LDS
+// and MFMAs: 64) where the plan's tiles are of 128 and one workgroup each
+// fills the GPU: 32 experts of 1536 x 2048 Q4_0, bf16, 64 / 96 / 128 tokens
+// each 49 / 52 / 85 us against 51 / 65 / 80 with TN 32.  Elsewhere TN 32:
+// 8 experts of 2048 x 4096, 16 / 48 / 96 tokens each 22 / 30 / 51 us.  There,
+// waves of a workgroup share rows (KG) while one per 32 rows and tile would
+// leave the GPU's SIMDs under one wave (16-bit activations, KG 4) or two (KG
+// 2): 101 tokens through 4096 x 14336 Q4_K took 352 / 262 / 257 us with KG 1
+// / 2 / 4.
 template <class F, class XT>
 int32_t launch_tile_n(const TileCall& c, hipStream_t st) {
-    constexpr int kWide = std::is_same<XT, float>::value ? 64 : 128;
-    const int tile = c.plan ? plan_tile(c.n_items, c.n_groups) : plan_tile(c.n_items, 1);
-    // waves that one per 32 rows and tile would be: a group's items on
-    // average, at most as many groups as items
+    constexpr bool kWideX = std::is_same<XT, float>::value;
+    constexpr int kWide = kWideX ? 64 : 128;
+    const int tile = plan_tile(c.n_items, c.plan ? c.n_groups : 1);
+    // a group's items on average; at most as many groups as items
     const int64_t groups = c.plan ? std::min<int64_t>(c.n_groups, c.n_items) : 1;
     const int64_t matrix_rows = c.swiglu ? 2 * c.rows : c.rows;
-    const int64_t wide = groups * ((c.n_items / groups + kWide - 1) / kWide) * ((matrix_rows + 127) / 128);
-    if (tile == 128 && wide >= device_cu_count()) return launch_tile_s<F, XT, kWide, 1>(c, tile, st);
-    if (tile == 128) return launch_tile_s<F, XT, 64, std::is_same<XT, float>::value ? 2 : 4>(c, tile, st);
-    const int64_t waves = groups * ((c.n_items / groups + 31) / 32) * ((matrix_rows + 31) / 32);
-    if constexpr (!std::is_same<XT, float>::value)
-        if (waves < 4 * device_cu_count() && !c.swiglu) return launch_tile_s<F, XT, 32, 4>(c, tile, st);
-    if (waves < 8 * device_cu_count()) return launch_tile_s<F, XT, 32, 2>(c, tile, st);
+    const int64_t each = c.n_items / groups, cus = device_cu_count();
+    const int64_t wide = groups * ((each + kWide - 1) / kWide) * ((matrix_rows + 127) / 128);
+    if (tile == 128 && wide >= cus) return launch_tile_s<F, XT, kWide, 1>(c, tile, st);
+    const int64_t waves = groups * ((each + 31) / 32) * ((matrix_rows + 31) / 32);
+    if constexpr (!kWideX) {
+        // 16 gate rows and 16 up rows in a wave: their bytes have to be
+        // within the 32-bit offsets from its first row
+        const bool near = !c.swiglu || c.rows * (c.cols / 32) < (1ll << 25);
+        if (waves < 4 * cus && near) return launch_tile_s<F, XT, 32, 4>(c, tile, st);
+    }
+    if (waves < 8 * cus) return launch_tile_s<F, XT, 32, 2>(c, tile, st);
     return launch_tile_s<F, XT, 32, 1>(c, tile, st);
 }
 

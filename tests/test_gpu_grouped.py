@@ -109,6 +109,58 @@ def test_product(env, fmt, x_name, T, S, E, rows, blocks):
         assert_close(got, y, e + (ov.rounded(np.abs(y) + e, y_name) if y_name != "f32" else 0), (fmt, y_name))
 
 
+@pytest.mark.parametrize("x_name", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("T,E,rows,blocks", [(300, 1, 16500, 3), (170, 2, 16500, 1), (60, 4, 17000, 2), (40, 2, 16500, 2),
+                                             (20, 1, 200, 43), (70, 1, 90, 11)])
+def test_every_tile_shape(env, fmt, x_name, T, E, rows, blocks):
+    """Shapes that take each tile: wide ones, narrow ones whose waves share rows or not, odd numbers of eight-block pieces."""
+    torch, qmv = env
+    K = blocks * (256 if fmt in ("q4_k", "q6_k") and blocks < 40 else 32 if fmt not in ("q4_k", "q6_k") else 256)
+    say("tiles", fmt, x_name, T, E, rows, K)
+    buf, stride, W = experts(fmt, f"t/grp/shape/{fmt}/{rows}/{K}", E, rows, K)
+    g = np.random.default_rng(T + E)
+    ids = g.integers(0, E, size=(T, 1))
+    xt, x = ov.as_type(torch, g.standard_normal((T, K)), x_name)
+    y, e = expect(fmt, W, rows, K, ids, x)
+    assert_close(run(torch, qmv, fmt, buf, stride, E, rows, K, ids, xt.cuda(), 1), y, e, fmt)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("x_name", ["f32", "f16"])
+@pytest.mark.parametrize("T,E,F", [(300, 1, 8300), (140, 2, 8300), (60, 4, 8500), (20, 1, 72)])
+def test_swiglu_in_every_tile_shape(env, fmt, x_name, T, E, F):
+    torch, qmv = env
+    H = 256
+    say("swiglu tiles", fmt, x_name, T, E, F)
+    buf, stride, W = experts(fmt, f"t/grp/gush/{fmt}/{F}", E, 2 * F, H)
+    g = np.random.default_rng(T)
+    ids = g.integers(0, E, size=(T, 1))
+    xt, x = ov.as_type(torch, 3 * g.standard_normal((T, H)), x_name)
+    a, ea = expect(fmt, W, 2 * F, H, ids, x)
+    h, eh = ov.swiglu(a[..., :F], ea[..., :F], a[..., F:], ea[..., F:])
+    plan = qmv.qmv_group_plan(torch.from_numpy(ids.astype(np.int32)).cuda(), E)
+    got = qmv.qmv_moe_grouped_swiglu(fmt, torch.from_numpy(buf).cuda(), stride, E, F, H, plan, 1, xt.cuda())
+    assert_close(got, h, eh, fmt)
+
+
+@pytest.mark.parametrize("fmt", ["q8_0", "q4_0", "q6_k"])
+def test_experts_two_bytes_past_a_word(env, fmt):
+    """Odd rows of an odd number of 2-byte-aligned units: every other expert starts 2 bytes past a word, the last ends there."""
+    torch, qmv = env
+    rows, E, T = 33, 4, 50
+    K = 256 if fmt == "q6_k" else 32 * 11
+    buf, stride, W = experts(fmt, f"t/grp/two/{fmt}", E, rows, K)
+    assert stride % 4 == 2 and buf.size % 4 == 0
+    for n in (E, E - 1):              # the buffer's end on a word, and 2 bytes past one
+        g = np.random.default_rng(n)
+        ids = g.integers(0, n, size=(T, 1))
+        xt, x = ov.as_type(torch, g.standard_normal((T, K)), "bf16")
+        y, e = expect(fmt, W[:n], rows, K, ids, x)
+        got = run(torch, qmv, fmt, buf[:(n - 1) * stride + W.shape[1]], stride, n, rows, K, ids, xt.cuda(), 1)
+        assert_close(got, y, e, (fmt, n))
+
+
 @pytest.mark.parametrize("fmt", FORMATS)
 def test_invalid_ids_give_nan_and_touch_nothing_else(env, fmt):
     torch, qmv = env

@@ -72,6 +72,18 @@ def test_against_64_bits(env, fmt, x_name, a_name, T, N, blocks, R, G):
     assert_close(c.run(torch, qmv), y, e)
 
 
+@pytest.mark.parametrize("x_name,a_name", [("f32", "f32"), ("f16", "f16"), ("bf16", "bf16")])
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("T,N,blocks,R,G", [(300, 16500, 1, 8, 3), (40, 2000, 9, 24, 40), (100, 600, 5, 72, 9)])
+def test_every_tile_shape(env, fmt, x_name, a_name, T, N, blocks, R, G):
+    torch, qmv = env
+    K = blocks * (256 if fmt in ("q4_k", "q6_k") else 32)
+    say("lora tiles", fmt, x_name, T, N, K, R, G)
+    c = Case(torch, fmt, T, N, K, R, G, x_name, a_name, seed=3)
+    y, e, _ = c.expect()
+    assert_close(c.run(torch, qmv), y, e)
+
+
 @pytest.mark.parametrize("T", [1, 7, 60, 260])
 def test_no_adapter_is_the_base_and_bad_ids_are_nan(env, T):
     torch, qmv = env
