@@ -430,8 +430,6 @@ __device__ __forceinline__ void store_y4(void* y, int y_type, int64_t at, f32x4 
     *reinterpret_cast<uint2*>(static_cast<uint16_t*>(y) + at) = uint2{w[0], w[1]};
 }
 
-constexpr int kTileWaves = 4;
-constexpr int kTileThreads = 64 * kTileWaves;
 constexpr int kLoraRanks = 64;                       // ranks staged at a time
 constexpr int kLoraPitch = 2 * kLoraRanks + 16;      // bytes of a token's piece, an odd number of 16-byte units
 
@@ -445,7 +443,7 @@ constexpr int kLoraPitch = 2 * kLoraRanks + 16;      // bytes of a token's piece
 // adapter (their sums meet in the epilogue).  An adapter's rows are loaded
 // while those of the one before are multiplied: 40 requests of 101 tokens
 // would else wait for 25 loads a tile, one after the other.
-template <int TN, int KG>
+template <int TN, int KG, int THREADS>
 __device__ __forceinline__ void add_adapters(const LoraTile& l, const int* s_adapter, int first, int count, int n_items,
                                              int rows, int row, int wk, uint8_t* lds, f32x16 (&acc)[TN / 32]) {
     constexpr int kSteps = kLoraRanks / 16;
@@ -455,11 +453,11 @@ __device__ __forceinline__ void add_adapters(const LoraTile& l, const int* s_ada
         const int steps = (ranks + 15) >> 4;
         __syncthreads();
         // fours of ranks, zeros past the last up to whole steps; all loads first
-        constexpr int kQuads = TN * 4 * kSteps / kTileThreads;
+        constexpr int kQuads = TN * 4 * kSteps / THREADS;
         f32x4 x[kQuads];
 #pragma unroll
         for (int q = 0; q < kQuads; ++q) {
-            const int i = tid + q * kTileThreads, j = i / (4 * kSteps), r = 4 * (i % (4 * kSteps));
+            const int i = tid + q * THREADS, j = i / (4 * kSteps), r = 4 * (i % (4 * kSteps));
             x[q] = f32x4{0.f, 0.f, 0.f, 0.f};
             if (j < count && r < ranks) {
                 const float* v = l.v + (int64_t)(first + j) * l.rank + c0 + r;
@@ -476,7 +474,7 @@ __device__ __forceinline__ void add_adapters(const LoraTile& l, const int* s_ada
         }
 #pragma unroll
         for (int q = 0; q < kQuads; ++q) {
-            const int i = tid + q * kTileThreads, j = i / (4 * kSteps), r = 4 * (i % (4 * kSteps));
+            const int i = tid + q * THREADS, j = i / (4 * kSteps), r = 4 * (i % (4 * kSteps));
 #pragma unroll
             for (int k = 0; k < 3; ++k) {
                 uint32_t w[2];
@@ -599,25 +597,40 @@ constexpr int kRowGroup = 32;     // compute units of an XCD: most row tiles of 
 // another's weights.  KG waves of a workgroup share 32 rows and take their
 // eight-block pieces of the row (four steps) in turn; their sums are added in
 // a fixed order at the end: where there are few rows, that keeps enough loads
-// in flight.  Activations are staged in LDS in chunks of CHS steps for each
-// of the KG.
+// in flight (KG 8 in workgroups of eight waves).  Activations are staged in
+// LDS in chunks of CHS steps for each of the KG.
 template <class F, class XT, int TN, int KG>
 struct TileShape {
     static constexpr int kP = XOp<XT>::kPieces;
-    static constexpr int kTM = 32 * kTileWaves / KG;
+    static constexpr int kWaves = KG > 4 ? KG : 4;
+    static constexpr int kThreads = 64 * kWaves;
+    static constexpr int kTM = 32 * kWaves / KG;
     static constexpr int kTS = TN / 32;
     static constexpr int kCHS = TN > 32 || kP > 1 || KG > 1 ? 1 : 2;
+    // Loads return in order, so a wait for activations that were asked for
+    // after a round's weights is a wait for those weights too.  With four
+    // chunks (a round) of activations on their way the weights have a round's
+    // time: 9 tokens through 4096 x 14336, KG 4: Q8_0 63 us against 97 with
+    // one chunk, Q4_K 72 against 94 with two.  That takes the third wave's
+    // registers, which KG 4 and 8 have no use for; at KG 2 it pays for Q8_0
+    // (101 tokens through 14336 x 4096 76 us against 96), not for Q4_K (78
+    // against 76) or Q6_K (95 against 89).
+    static constexpr bool kDeep = kP == 1 && (KG > 2 || (KG == 2 && Unit<F>::kCpr > 14));
     // waves of a SIMD that the registers are cut for; few tokens leave the
-    // decoding as the bound, and it takes four waves to keep that going
-    static constexpr int kOcc = TN > 32 || kP > 1 ? 2 : 3;
+    // decoding as the bound, and it takes more waves to keep that going.
+    // fp32 pieces with KG 4 fill the LDS with one workgroup
+    static constexpr int kOcc = kP > 1 && KG > 2 ? 1 : TN > 32 || kP > 1 || kDeep ? 2 : 3;
     // whether a step is decoded during the one before it; for few tokens
     // Q6_K's words and a second set of operands would take the third wave
     // (64 tokens through 128 experts 180 us against 200)
     static constexpr bool kAhead = TN > 32 || Unit<F>::kSub == 1;
     static constexpr int kCH = kCHS * KG;
     // chunks of activations on their way besides the one being staged
-    static constexpr int kXAhead = TN < 128 && kP == 1 && Unit<F>::kCpr <= 10 ? 2 : 1;      // as registers allow
-    static constexpr int kXL = TN * 8 * kCH / kTileThreads;         // 8-column pieces of x per thread and chunk
+    static constexpr int kXAhead = kDeep                                                 ? 4
+                                   : kP > 1 && KG > 2                                    ? 2
+                                   : TN < 128 && kP == 1 && Unit<F>::kCpr <= 10          ? 2
+                                                                                         : 1;     // as registers allow
+    static constexpr int kXL = TN * 8 * kCH / kThreads;         // 8-column pieces of x per thread and chunk
     static constexpr int kPitch = 128 * kCH + 16;                   // bytes of a staged token: an odd number of 16-byte units, so 8 tokens hit distinct banks
     static constexpr int kX = kP * TN * kPitch;
     static constexpr int kM = Unit<F>::kSums ? 2 * kCH * TN * 16 : 0;
@@ -625,7 +638,7 @@ struct TileShape {
     static constexpr int kSlot = 32 * Unit<F>::kPitch;              // of a wave
     static constexpr int kOutPitch = kTM + 4;                       // floats
     static constexpr int kOut = KG * TN * kOutPitch * 4;
-    static constexpr int kMain = 2 * kBuf + kTileWaves * kSlot;
+    static constexpr int kMain = 2 * kBuf + kWaves * kSlot;
     static constexpr int kLora = 3 * TN * kLoraPitch;
     static constexpr int kLds = kMain > kOut ? kMain : kOut;
     static_assert(kXL >= 1 && kCHS >= 1, "every thread stages, every wave computes");
@@ -633,7 +646,8 @@ struct TileShape {
 
 // LORA: the tokens carry adapters (and there is no plan).
 template <class F, class XT, int TN, int KG, bool LORA>
-__global__ __launch_bounds__(kTileThreads, (TileShape<F, XT, TN, KG>::kOcc)) void tile_kernel(const TileDev a) {
+__global__ __launch_bounds__((TileShape<F, XT, TN, KG>::kThreads), (TileShape<F, XT, TN, KG>::kOcc)) void tile_kernel(
+    const TileDev a) {
     using S = TileShape<F, XT, TN, KG>;
     using U = Unit<F>;
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
@@ -749,7 +763,7 @@ __global__ __launch_bounds__(kTileThreads, (TileShape<F, XT, TN, KG>::kOcc)) voi
     }
     __syncthreads();
     if (a.plan && group >= a.n_groups) {   // ids that are no group
-        for (int i = tid; i < count * out_rows; i += kTileThreads) {
+        for (int i = tid; i < count * out_rows; i += S::kThreads) {
             const int r = row0 + i % out_rows;
             if (r < a.rows)
                 store_y(a.y, a.y_type, (int64_t)s_item[i / out_rows] * a.ldy + r, __builtin_nanf(""));
@@ -761,7 +775,7 @@ __global__ __launch_bounds__(kTileThreads, (TileShape<F, XT, TN, KG>::kOcc)) voi
     // tokens.  Chunk c is steps kCHS (c % (4 / kCHS)).. of round c / (4 / kCHS).
     const int xc = tid % (8 * S::kCH), xt = tid / (8 * S::kCH);
     const int xk = xc / (8 * S::kCHS), xw = xc % (8 * S::kCHS);
-    constexpr int kXStep = kTileThreads / (8 * S::kCH);
+    constexpr int kXStep = S::kThreads / (8 * S::kCH);
     constexpr int kParts = 4 / S::kCHS;
     const XT* xp[S::kXL];
 #pragma unroll
@@ -955,8 +969,8 @@ __global__ __launch_bounds__(kTileThreads, (TileShape<F, XT, TN, KG>::kOcc)) voi
         for (int k = 0; k < S::kXAhead; ++k)
 #pragma unroll
             for (int i = 0; i < S::kXL; ++i) gx[k].x[i].zero();       // tokens past the tile's stay 0
-        load_x(0, gx[0]);
-        if constexpr (S::kXAhead > 1) load_x(1, gx[1]);
+#pragma unroll
+        for (int k = 0; k < S::kXAhead; ++k) load_x(k, gx[k]);
         auto decode = [&](auto jc, int s, Ops& o) __attribute__((always_inline)) {
             decode_scales(jc, s, o);
             static_for(std::make_integer_sequence<int, 4>{},
@@ -1007,8 +1021,8 @@ __global__ __launch_bounds__(kTileThreads, (TileShape<F, XT, TN, KG>::kOcc)) voi
         }
     }
     if constexpr (LORA)
-        add_adapters<TN, KG>(a.lora, s_adapter, start, count, a.n_items, a.rows, min(row0 + wr + lr, a.rows - 1), wk, lds,
-                             acc);
+        add_adapters<TN, KG, S::kThreads>(a.lora, s_adapter, start, count, a.n_items, a.rows,
+                                          min(row0 + wr + lr, a.rows - 1), wk, lds, acc);
     __syncthreads();
 
     // results through LDS, so that stores run along the rows
@@ -1021,7 +1035,7 @@ __global__ __launch_bounds__(kTileThreads, (TileShape<F, XT, TN, KG>::kOcc)) voi
     __syncthreads();
     // four rows a thread; rows of a tile are a power of two
     const int quads = out_rows >> 2, qshift = __builtin_ctz(quads);
-    for (int i = tid; i < count << qshift; i += kTileThreads) {
+    for (int i = tid; i < count << qshift; i += S::kThreads) {
         const int j = i >> qshift, r = (i & (quads - 1)) << 2;
         auto result = [&](int rr) __attribute__((always_inline)) {
             f32x4 v = *reinterpret_cast<const f32x4*>(out + j * S::kOutPitch + rr);
@@ -1086,7 +1100,7 @@ int32_t launch_tile(const TileCall& c, int plan_tile, hipStream_t st) {
     if (const int32_t e = lds_limit(reinterpret_cast<const void*>(kern), kLdsMax, "qmv", &dyn_max)) return e;
     const size_t lds = std::max<size_t>(S::kLds, LORA ? S::kLora : 0);
     if (lds > dyn_max) return fail(QMV_EHIP, "qmv: the tile kernel's LDS exceeds the device's");
-    hipLaunchKernelGGL(kern, dim3((unsigned)grid), dim3(kTileThreads), lds, st, d);
+    hipLaunchKernelGGL(kern, dim3((unsigned)grid), dim3(S::kThreads), lds, st, d);
     return check_launch("qmv");
 }
 
@@ -1100,10 +1114,16 @@ int32_t launch_tile_s(const TileCall& c, int tile, hipStream_t st) {
 // fills the GPU: 32 experts of 1536 x 2048 Q4_0, bf16, 64 / 96 / 128 tokens
 // each 49 / 52 / 85 us against 51 / 65 / 80 with TN 32.  Elsewhere TN 32:
 // 8 experts of 2048 x 4096, 16 / 48 / 96 tokens each 22 / 30 / 51 us.  There,
-// waves of a workgroup share rows (KG) while one per 32 rows and tile would
-// leave the GPU's SIMDs under one wave (16-bit activations, KG 4) or two (KG
-// 2): 101 tokens through 4096 x 14336 Q4_K took 352 / 262 / 257 us with KG 1
-// / 2 / 4.
+// waves of a workgroup share rows (KG) where one per 32 rows and tile would
+// leave the GPU's SIMDs short of waves.  16-bit activations, at most a wave
+// per compute unit: KG 8 (9 tokens through 4096 x 14336: Q8_0 55 us against
+// 63 with KG 4, Q4_K 58 against 72; with 1.75 waves, 14336 x 4096 Q8_0, KG 4
+// 37 against 49); under one a SIMD: KG 4 (101 tokens through 4096 x 14336
+// Q4_K 262 / 257 us with KG 2 / 4, before the loads below); under two: KG 2
+// (352 with KG 1).  fp32, whose pieces take three times the LDS: at most a
+// wave per compute unit KG 4 (9 tokens, 4096 x 14336 Q8_0 87 us against 127
+// with KG 2), else KG 2 (101 tokens, 8192 x 4096 Q4_0 50 us against 73 with
+// KG 1).
 template <class F, class XT>
 int32_t launch_tile_n(const TileCall& c, hipStream_t st) {
     constexpr bool kWideX = std::is_same<XT, float>::value;
@@ -1116,10 +1136,13 @@ int32_t launch_tile_n(const TileCall& c, hipStream_t st) {
     const int64_t wide = groups * ((each + kWide - 1) / kWide) * ((matrix_rows + 127) / 128);
     if (tile == 128 && wide >= cus) return launch_tile_s<F, XT, kWide, 1>(c, tile, st);
     const int64_t waves = groups * ((each + 31) / 32) * ((matrix_rows + 31) / 32);
-    if constexpr (!kWideX) {
-        // 16 gate rows and 16 up rows in a wave: their bytes have to be
-        // within the 32-bit offsets from its first row
-        const bool near = !c.swiglu || c.rows * (c.cols / 32) < (1ll << 25);
+    // KG 4 and 8 have 16 gate rows and 16 up rows in a wave: their bytes have
+    // to be within the 32-bit offsets from its first row
+    const bool near = !c.swiglu || c.rows * (c.cols / 32) < (1ll << 25);
+    if constexpr (kWideX) {
+        if (waves <= cus && near) return launch_tile_s<F, XT, 32, 4>(c, tile, st);
+    } else {
+        if (waves <= cus && near) return launch_tile_s<F, XT, 32, 8>(c, tile, st);
         if (waves < 4 * cus && near) return launch_tile_s<F, XT, 32, 4>(c, tile, st);
     }
     if (waves < 8 * cus) return launch_tile_s<F, XT, 32, 2>(c, tile, st);

@@ -112,7 +112,7 @@ def test_product(env, fmt, x_name, T, S, E, rows, blocks):
 @pytest.mark.parametrize("x_name", ["f32", "f16", "bf16"])
 @pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("T,E,rows,blocks", [(300, 1, 16500, 3), (170, 2, 16500, 1), (60, 4, 17000, 2), (40, 2, 16500, 2),
-                                             (20, 1, 200, 43), (70, 1, 90, 11)])
+                                             (20, 1, 200, 43), (70, 1, 90, 11), (40, 1, 9000, 9), (33, 1, 4500, 37)])
 def test_every_tile_shape(env, fmt, x_name, T, E, rows, blocks):
     """Shapes that take each tile: wide ones, narrow ones whose waves share rows or not, odd numbers of eight-block pieces."""
     torch, qmv = env
@@ -128,7 +128,8 @@ def test_every_tile_shape(env, fmt, x_name, T, E, rows, blocks):
 
 @pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("x_name", ["f32", "f16"])
-@pytest.mark.parametrize("T,E,F", [(300, 1, 8300), (140, 2, 8300), (60, 4, 8500), (20, 1, 72)])
+@pytest.mark.parametrize("T,E,F", [(300, 1, 8300), (140, 2, 8300), (60, 4, 8500), (20, 1, 72),
+                                   (20, 1, 8500), (60, 2, 8500)])
 def test_swiglu_in_every_tile_shape(env, fmt, x_name, T, E, F):
     torch, qmv = env
     H = 256
