@@ -13,8 +13,11 @@
 // of the vocabulary; (2) the decisions, made alike by every workgroup of a
 // request, and the chunk sums of the drawn row's weights; (3) the chunk and
 // the place in it.  (3) by the last workgroup of (2) took longer: the fences
-// it needs write the L2s back (139 us against 26 + 27 for 64 requests of
-// 151936 tokens).  Exponentials and sums are in
+// it needs write the L2s back (139 us against 26 + 27 with the same bodies
+// for 64 requests of 151936 tokens).  There the three take 46, 22 and 11 us;
+// the first is bound by memory (fp32 logits of 64 x 1..8 rows at the copy
+// rate), the others by fp64 exponentials and by latency: 1 request of 4
+// drafts and 128256 tokens takes 4, 7 and 8 us.  Exponentials and sums are in
 // fp64: the outputs are comparisons, and with fp32 sums (1e-7 off) over a
 // vocabulary of 1.5e5 about one draw in thirty could fall on the wrong side
 // of a border between two tokens of mean mass.
@@ -46,7 +49,7 @@ struct VerifyArgs {
     int D, V, chunks, vec, qvec;
     double2* part;         // [requests][D + 1][chunks]: maximum, sum of exp(l - maximum)
     double2* sums;         // [requests][chunks]: sum of max(p - q, 0), sum of p, times the row's sum
-    Decision* made; // [requests]
+    Decision* made;        // [requests]
     int32_t* tokens;
     int32_t* kept;
 };
