@@ -61,7 +61,7 @@ def run(torch, qmv, fmt, buf, stride, E, rows, K, ids, x, top_k, **kw):
 
 # ------------------------------------------------------------------ the plan
 @pytest.mark.parametrize("n,E", [(1, 1), (7, 3), (64, 1024), (1023, 5), (1024, 128), (1025, 128), (5000, 37), (40000, 1024),
-                                 (16384, 128), (16385, 128), (20000, 8)])
+                                 (16384, 128), (16385, 128), (20000, 8), (200001, 300)])
 @pytest.mark.parametrize("kind", ["even", "one", "bad"])
 def test_plan_is_a_stable_sort(env, n, E, kind):
     torch, qmv = env
