@@ -496,7 +496,8 @@ int32_t qmv_group_plan(const int32_t* group_ids, int64_t n_items, int32_t n_grou
  * Codes are exact in the matrix cores' types, 16-bit activations too, and
  * fp32 activations are split into three bf16 pieces (24 bits); sums and
  * scales are fp32: the accuracy contract holds as for the matvec.  An item's
- * outputs do not depend on the other items.
+ * outputs do not depend on the other items' values; how many items there are
+ * can change the order of the fp32 sums.
  * Errors: QMV_EINVAL, QMV_EALIGN, QMV_EUNSUPPORTED (unknown fmt), QMV_EHIP.
  */
 int32_t qmv_moe_grouped(qmv_fmt fmt, const void* W_experts, int64_t expert_stride_bytes, int32_t n_experts,
@@ -539,8 +540,10 @@ int32_t qmv_moe_weighted_sum(const void* y, int32_t y_type, const float* weights
  *   workspace  device memory of >= qmv_lora_workspace_bytes(...) bytes,
  *            16-byte aligned; any contents; calls that share one must not
  *            run concurrently.
- * The base is the matvec's result up to 8 tokens; the adapters' products and
- * sums are fp32.  A token's outputs do not depend on other tokens' adapters.
+ * The base is the matvec's result up to 8 tokens (fp32 x: the FMA kernels',
+ * QMV_PATH_FMA); the adapters' products and sums are fp32.  The same call
+ * gives the same bits; the other tokens' number and adapters can change the
+ * order of a token's fp32 sums, nothing else.
  * Errors: QMV_EINVAL, QMV_EALIGN, QMV_EUNSUPPORTED (unknown fmt), QMV_EHIP.
  */
 size_t qmv_lora_workspace_bytes(int64_t n_tokens, int32_t rank, int32_t n_adapters);
