@@ -470,22 +470,14 @@ class GroupPlan:
 # The calls below run once a layer or a step for a few microseconds of GPU
 # time, so their checks are kept short: one comparison of all that a tensor
 # has to be, and the words for what is wrong only where it is.
-_types = {}          # torch dtype -> x_type, filled at the first call
-_empty = None
-
-
-def _setup():
-    global _empty
-    torch = _torch()
-    _types.update(_x_types(torch))
-    _empty = torch.empty
-    return torch
+_types = None        # torch dtype -> x_type; set whole at the first call, which any thread may make
 
 
 def _type_of(t, name):
     """x_type of a float GPU tensor."""
-    if not _types:
-        _setup()
+    global _types
+    if _types is None:
+        _types = _x_types(_torch())
     xt = _types.get(getattr(t, "dtype", None))
     if xt is None or not t.is_cuda:
         torch = _torch()
@@ -517,7 +509,7 @@ def _scratch(buf, name, need, like, stream):
     """A caller's uint8 buffer of at least `need` bytes, or a new one, kept
     from reuse until a stream other than the current one is done with it."""
     if buf is None:
-        buf = _empty(need or 16, dtype=_torch().uint8, device=like.device)
+        buf = _torch().empty(need or 16, dtype=_torch().uint8, device=like.device)
         if stream is not None:
             buf.record_stream(stream)
     else:
@@ -537,7 +529,7 @@ def qmv_group_plan(group_ids, n_groups, plan=None, stream=None):
     by group and returns the GroupPlan that the grouped products take.  plan:
     a uint8 GPU tensor to build it in (its size: the library's
     qmv_group_plan_bytes), or None for a new one."""
-    torch = _torch() if _types else _setup()
+    torch = _torch()
     ids = _full(group_ids, "group_ids", torch.int32, getattr(group_ids, "shape", None))
     n = group_ids.numel()
     buf = _scratch(plan, "plan", _lib.qmv_group_plan_bytes(n, n_groups), group_ids, stream)
@@ -559,7 +551,8 @@ def _grouped(cfn, fmt, W, stride, E, rows, matrix_rows, cols, plan, top_k, x, ou
     if not isinstance(plan, GroupPlan) or plan.n_items != T * top_k or plan.n_groups != E:
         raise ValueError(f"plan must be qmv_group_plan's of {T * top_k} items and {E} groups")
     if out is None:
-        out = _empty((T, top_k, rows), dtype=dtype or _torch().float32, device=x.device)
+        torch = _torch()
+        out = torch.empty((T, top_k, rows), dtype=dtype or torch.float32, device=x.device)
         ot = _type_of(out, name)
     else:
         ot = _type_of(out, name)
@@ -600,7 +593,7 @@ def qmv_moe_weighted_sum(y, weights, out=None, out_dtype=None, stream=None):
     T, S, N = y.shape
     w = _full(weights, "weights", torch.float32, (T, S))
     if out is None:
-        out = _empty((T, N), dtype=out_dtype or torch.float32, device=y.device)
+        out = torch.empty((T, N), dtype=out_dtype or torch.float32, device=y.device)
         ot = _type_of(out, "out")
     else:
         ot = _type_of(out, "out")
@@ -632,7 +625,7 @@ def qmv_lora(fmt, W, n_rows, n_cols, x, A, B, scales, adapter_ids, y=None, works
     s = _full(scales, "scales", torch.float32, (G,))
     ids = _full(adapter_ids, "adapter_ids", torch.int32, (T,))
     if y is None:
-        y = _empty((T, n_rows), dtype=torch.float32, device=x.device)
+        y = torch.empty((T, n_rows), dtype=torch.float32, device=x.device)
         ldy = n_rows
     else:
         _dev(y, "y", torch.float32)
@@ -673,11 +666,11 @@ def qmv_spec_verify(logits, draft_probs, draft_tokens, n_draft, u_accept, u_last
     x, n = _full(draft_tokens, "draft_tokens", i32, (Q, D)), _full(n_draft, "n_draft", i32, (Q,))
     u, ul = _full(u_accept, "u_accept", f32, (Q, D)), _full(u_last, "u_last", f32, (Q,))
     if tokens is None:
-        tokens = _empty((Q, D1), dtype=i32, device=logits.device)
+        tokens = torch.empty((Q, D1), dtype=i32, device=logits.device)
     else:
         _full(tokens, "tokens", i32, (Q, D1))
     if n_kept is None:
-        n_kept = _empty((Q,), dtype=i32, device=logits.device)
+        n_kept = torch.empty((Q,), dtype=i32, device=logits.device)
     else:
         _full(n_kept, "n_kept", i32, (Q,))
     ws = _scratch(workspace, "workspace", _lib.qmv_spec_verify_workspace_bytes(Q, D, V), logits, stream)
