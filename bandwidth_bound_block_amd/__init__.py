@@ -8,6 +8,11 @@ Every step of the computation runs in the library's kernels; there is no
 fallback of any kind, and importing this package fails loudly when the
 library has not been built.
 
+A call runs on `stream`, or on the current stream.  The tensors that it makes
+(outputs, workspaces) come from that stream's pool.  As for any work on
+another stream, the caller has it wait for what makes the inputs, waits for
+it before the outputs are read, and keeps the inputs until it is done.
+
 Entry points (same names as the C ABI):
   qmv_q8_0 / qmv_q4_0 / qmv_q4_1   float block-quantized matvec, batch 1..8
   qmv_q4_k                         the same for Q4_K super-blocks (256 weights, 144 bytes)
@@ -195,6 +200,26 @@ def _dev(t, name, dtype):
     return t
 
 
+def _new(shape, dtype, like, stream, returned=True):
+    """A new tensor on like's device for a call on `stream` (None: the current
+    stream), from the pool of that stream.  A block of the current stream's
+    pool may still be in use by work queued there, which another stream does
+    not wait for, and would go back there while that stream still writes it.
+    A tensor that is returned is read on the current stream too, once that
+    has waited, and does not go back before."""
+    torch = _torch()
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    here = torch.cuda.current_stream(like.device)
+    if stream.cuda_stream == here.cuda_stream:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=like.device)
+    if returned:
+        t.record_stream(here)
+    return t
+
+
 def _rows2d(t, name, K):
     """[K] or [B, K] with unit inner stride -> (tensor2d, B, ld)."""
     t2 = t.unsqueeze(0) if t.dim() == 1 else t
@@ -216,7 +241,7 @@ def _matvec(cfn, fmt, W, n_rows, n_cols, x, y, stream):
         raise ValueError(f"W must be contiguous and hold {need} bytes")
     x2, B, ldx = _rows2d(x, "x", n_cols)
     if y is None:
-        y = torch.empty((B, n_rows), dtype=torch.float32, device=x.device)
+        y = _new((B, n_rows), torch.float32, x, stream)
     _dev(y, "y", torch.float32)
     y2, By, ldy = _rows2d(y, "y", n_rows)
     if By != B:
@@ -282,7 +307,7 @@ def qmv_matvec_xt(fmt, W, n_rows, n_cols, x, path=PATH_AUTO, y=None, stream=None
         raise ValueError(f"W must be contiguous and hold {need} bytes")
     x2, B, ldx = _rows2d(x, "x", n_cols)
     if y is None:
-        y = torch.empty((B, n_rows), dtype=torch.float32, device=x.device)
+        y = _new((B, n_rows), torch.float32, x, stream)
     _dev(y, "y", torch.float32)
     y2, By, ldy = _rows2d(y, "y", n_rows)
     if By != B:
@@ -317,7 +342,7 @@ def _i8(W, x, mult, shift, lut, y, stream):
         raise ValueError("mult and shift must be contiguous [N]")
     x2, B, ldx = _rows2d(x, "x", K)
     if y is None:
-        y = torch.empty((B, N), dtype=torch.int8, device=x.device)
+        y = _new((B, N), torch.int8, x, stream)
     _dev(y, "y", torch.int8)
     y2, By, ldy = _rows2d(y, "y", N)
     if By != B:
@@ -372,7 +397,7 @@ def qmv_moe_xt(fmt, W_experts, expert_stride_bytes, n_experts, n_rows, n_cols, e
     torch, fmt, B, T, st_tok, st_slot = _moe_args(fmt, W_experts, expert_stride_bytes, n_experts, n_rows, n_cols,
                                                   expert_ids, x, xt)
     if y is None:
-        y = torch.empty((B, T, n_rows), dtype=torch.float32, device=x.device)
+        y = _new((B, T, n_rows), torch.float32, x, stream)
     _dev(y, "y", torch.float32)
     if y.shape != (B, T, n_rows) or not y.is_contiguous():
         raise ValueError("y must be a contiguous [B, top_k, n_rows] tensor")
@@ -390,7 +415,7 @@ def qmv_moe_swiglu_xt(fmt, W_experts, expert_stride_bytes, n_experts, n_ff, n_co
     torch, fmt, B, T, st_tok, st_slot = _moe_args(fmt, W_experts, expert_stride_bytes, n_experts, 2 * n_ff, n_cols,
                                                   expert_ids, x, xt)
     if h is None:
-        h = torch.empty((B, T, n_ff), dtype=torch.float32, device=x.device)
+        h = _new((B, T, n_ff), torch.float32, x, stream)
     _dev(h, "h", torch.float32)
     if h.shape != (B, T, n_ff) or not h.is_contiguous():
         raise ValueError("h must be a contiguous [B, top_k, n_ff] tensor")
@@ -408,7 +433,7 @@ def qmv_moe_swiglu(fmt, W_experts, expert_stride_bytes, n_experts, n_ff, n_cols,
     torch, fmt, B, T, st_tok, st_slot = _moe_args(fmt, W_experts, expert_stride_bytes, n_experts, 2 * n_ff, n_cols,
                                                   expert_ids, x)
     if h is None:
-        h = torch.empty((B, T, n_ff), dtype=torch.float32, device=x.device)
+        h = _new((B, T, n_ff), torch.float32, x, stream)
     _dev(h, "h", torch.float32)
     if h.shape != (B, T, n_ff) or not h.is_contiguous():
         raise ValueError("h must be a contiguous [B, top_k, n_ff] tensor")
@@ -429,7 +454,7 @@ def qmv_moe_combine(fmt, W_experts, expert_stride_bytes, n_experts, n_rows, n_co
     if weights.shape != (B, T) or not weights.is_contiguous():
         raise ValueError("weights must be a contiguous [B, top_k] tensor")
     if out is None:
-        out = torch.empty((B, n_rows), dtype=torch.float32, device=x.device)
+        out = _new((B, n_rows), torch.float32, x, stream)
     _dev(out, "out", torch.float32)
     if out.shape != (B, n_rows) or not out.is_contiguous():
         raise ValueError("out must be a contiguous [B, n_rows] tensor")
@@ -449,7 +474,7 @@ def qmv_moe(fmt, W_experts, expert_stride_bytes, n_experts, n_rows, n_cols, expe
     torch, fmt, B, T, st_tok, st_slot = _moe_args(fmt, W_experts, expert_stride_bytes, n_experts, n_rows, n_cols,
                                                   expert_ids, x)
     if y is None:
-        y = torch.empty((B, T, n_rows), dtype=torch.float32, device=x.device)
+        y = _new((B, T, n_rows), torch.float32, x, stream)
     _dev(y, "y", torch.float32)
     if y.shape != (B, T, n_rows) or not y.is_contiguous():
         raise ValueError("y must be a contiguous [B, top_k, n_rows] tensor")
@@ -505,15 +530,11 @@ def _bytes_of(t, name, need):
     return t.data_ptr()
 
 
-def _scratch(buf, name, need, like, stream):
-    """A caller's uint8 buffer of at least `need` bytes, or a new one, kept
-    from reuse until a stream other than the current one is done with it."""
+def _scratch(buf, name, need, like, stream, returned=False):
+    """A caller's uint8 buffer of at least `need` bytes, or a new one."""
     if buf is None:
-        buf = _torch().empty(need or 16, dtype=_torch().uint8, device=like.device)
-        if stream is not None:
-            buf.record_stream(stream)
-    else:
-        _bytes_of(buf, name, need)
+        return _new((need or 16,), _torch().uint8, like, stream, returned)
+    _bytes_of(buf, name, need)
     return buf
 
 
@@ -532,7 +553,7 @@ def qmv_group_plan(group_ids, n_groups, plan=None, stream=None):
     torch = _torch()
     ids = _full(group_ids, "group_ids", torch.int32, getattr(group_ids, "shape", None))
     n = group_ids.numel()
-    buf = _scratch(plan, "plan", _lib.qmv_group_plan_bytes(n, n_groups), group_ids, stream)
+    buf = _scratch(plan, "plan", _lib.qmv_group_plan_bytes(n, n_groups), group_ids, stream, True)
     _check(_lib.qmv_group_plan(ids, n, n_groups, buf.data_ptr(), buf.numel(), _on(stream, group_ids)))
     return GroupPlan(buf, n, n_groups)
 
@@ -551,8 +572,7 @@ def _grouped(cfn, fmt, W, stride, E, rows, matrix_rows, cols, plan, top_k, x, ou
     if not isinstance(plan, GroupPlan) or plan.n_items != T * top_k or plan.n_groups != E:
         raise ValueError(f"plan must be qmv_group_plan's of {T * top_k} items and {E} groups")
     if out is None:
-        torch = _torch()
-        out = torch.empty((T, top_k, rows), dtype=dtype or torch.float32, device=x.device)
+        out = _new((T, top_k, rows), dtype or _torch().float32, x, stream)
         ot = _type_of(out, name)
     else:
         ot = _type_of(out, name)
@@ -593,7 +613,7 @@ def qmv_moe_weighted_sum(y, weights, out=None, out_dtype=None, stream=None):
     T, S, N = y.shape
     w = _full(weights, "weights", torch.float32, (T, S))
     if out is None:
-        out = torch.empty((T, N), dtype=out_dtype or torch.float32, device=y.device)
+        out = _new((T, N), out_dtype or torch.float32, y, stream)
         ot = _type_of(out, "out")
     else:
         ot = _type_of(out, "out")
@@ -625,7 +645,7 @@ def qmv_lora(fmt, W, n_rows, n_cols, x, A, B, scales, adapter_ids, y=None, works
     s = _full(scales, "scales", torch.float32, (G,))
     ids = _full(adapter_ids, "adapter_ids", torch.int32, (T,))
     if y is None:
-        y = torch.empty((T, n_rows), dtype=torch.float32, device=x.device)
+        y = _new((T, n_rows), torch.float32, x, stream)
         ldy = n_rows
     else:
         _dev(y, "y", torch.float32)
@@ -666,11 +686,11 @@ def qmv_spec_verify(logits, draft_probs, draft_tokens, n_draft, u_accept, u_last
     x, n = _full(draft_tokens, "draft_tokens", i32, (Q, D)), _full(n_draft, "n_draft", i32, (Q,))
     u, ul = _full(u_accept, "u_accept", f32, (Q, D)), _full(u_last, "u_last", f32, (Q,))
     if tokens is None:
-        tokens = torch.empty((Q, D1), dtype=i32, device=logits.device)
+        tokens = _new((Q, D1), i32, logits, stream)
     else:
         _full(tokens, "tokens", i32, (Q, D1))
     if n_kept is None:
-        n_kept = torch.empty((Q,), dtype=i32, device=logits.device)
+        n_kept = _new((Q,), i32, logits, stream)
     else:
         _full(n_kept, "n_kept", i32, (Q,))
     ws = _scratch(workspace, "workspace", _lib.qmv_spec_verify_workspace_bytes(Q, D, V), logits, stream)
@@ -685,7 +705,7 @@ def qmv_dequant(fmt, W, n_rows, n_cols, out=None, stream=None):
     fmt = _fmt(fmt)
     _dev(W, "W", torch.uint8)
     if out is None:
-        out = torch.empty((n_rows, n_cols), dtype=torch.float32, device=W.device)
+        out = _new((n_rows, n_cols), torch.float32, W, stream)
     _dev(out, "out", torch.float32)
     if out.shape != (n_rows, n_cols) or not out.is_contiguous():
         raise ValueError("out must be a contiguous [n_rows, n_cols] tensor")
