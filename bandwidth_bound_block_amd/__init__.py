@@ -485,11 +485,12 @@ def qmv_moe(fmt, W_experts, expert_stride_bytes, n_experts, n_rows, n_cols, expe
 
 
 class GroupPlan:
-    """Items sorted by group (qmv_group_plan): the device buffer and its sizes."""
-    __slots__ = ("buffer", "n_items", "n_groups")
+    """Items sorted by group (qmv_group_plan): the device buffer and its sizes,
+    and the HIP stream whose pool the buffer is from (None: not known)."""
+    __slots__ = ("buffer", "n_items", "n_groups", "stream")
 
-    def __init__(self, buffer, n_items, n_groups):
-        self.buffer, self.n_items, self.n_groups = buffer, n_items, n_groups
+    def __init__(self, buffer, n_items, n_groups, stream=None):
+        self.buffer, self.n_items, self.n_groups, self.stream = buffer, n_items, n_groups, stream
 
 
 # The calls below run once a layer or a step for a few microseconds of GPU
@@ -554,8 +555,9 @@ def qmv_group_plan(group_ids, n_groups, plan=None, stream=None):
     ids = _full(group_ids, "group_ids", torch.int32, getattr(group_ids, "shape", None))
     n = group_ids.numel()
     buf = _scratch(plan, "plan", _lib.qmv_group_plan_bytes(n, n_groups), group_ids, stream, True)
-    _check(_lib.qmv_group_plan(ids, n, n_groups, buf.data_ptr(), buf.numel(), _on(stream, group_ids)))
-    return GroupPlan(buf, n, n_groups)
+    on = _on(stream, group_ids)
+    _check(_lib.qmv_group_plan(ids, n, n_groups, buf.data_ptr(), buf.numel(), on))
+    return GroupPlan(buf, n, n_groups, on if plan is None else None)
 
 
 def _grouped(cfn, fmt, W, stride, E, rows, matrix_rows, cols, plan, top_k, x, out, name, dtype, stream):
@@ -577,8 +579,11 @@ def _grouped(cfn, fmt, W, stride, E, rows, matrix_rows, cols, plan, top_k, x, ou
     else:
         ot = _type_of(out, name)
         _full(out, name, out.dtype, (T, top_k, rows))
+    on = _on(stream, x)
+    if plan.stream != on:      # its memory goes back to another stream's pool: not while this one reads it
+        plan.buffer.record_stream(_torch().cuda.current_stream(x.device) if stream is None else stream)
     _check(cfn(f, w, stride, E, rows, cols, plan.buffer.data_ptr(), T, top_k, x.data_ptr(), xt, st_tok, st_slot,
-               out.data_ptr(), ot, _on(stream, x)))
+               out.data_ptr(), ot, on))
     return out
 
 

@@ -132,3 +132,31 @@ def test_an_output_dropped_while_the_current_stream_reads_it(env, made):
     assert all(t.data_ptr() != at for t in more)
     torch.cuda.synchronize()
     assert torch.equal(copy.cpu(), want)
+
+
+def test_a_plan_used_on_another_stream(env):
+    torch, qmv = env
+    E, N, K, T = 4, 64, 256, 50
+    g = torch.Generator().manual_seed(1)
+    W = torch.from_numpy(wl.quant_weights("q4_0", "t/streams/plan", E * N, K).reshape(-1)).cuda()
+    stride = N * qmv.row_bytes("q4_0", K)
+    ids = torch.randint(0, E, (T, 1), generator=g, dtype=torch.int32).cuda()
+    x = torch.randn(T, K, generator=g).cuda()
+    want = qmv.qmv_moe_grouped("q4_0", W, stride, E, N, K, qmv.qmv_group_plan(ids, E), 1, x).cpu()
+    busy = torch.randn(4096, 4096, generator=g).cuda()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    plan = qmv.qmv_group_plan(ids, E)
+    size = plan.buffer.numel()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        m = busy
+        for _ in range(20):
+            m = m @ busy * 0.01
+    got = qmv.qmv_moe_grouped("q4_0", W, stride, E, N, K, plan, 1, x, stream=side)
+    at = plan.buffer.data_ptr()
+    del plan
+    others = [torch.zeros(size, dtype=torch.uint8, device="cuda") for _ in range(4)]     # while the product has not begun
+    assert all(t.data_ptr() != at for t in others)
+    torch.cuda.synchronize()
+    assert np.array_equal(got.cpu().numpy(), want.numpy())

@@ -179,3 +179,27 @@ def test_nothing_is_recorded_on_the_current_stream(stand, name, given):
     CALLS[name](qmv, st.main if given else None)
     assert st.made and all(t.pool is st.main and not hasattr(t, "recorded") for t in st.made)
     assert all(getattr(s, "value", s) == 11 for _, s in st.calls)
+
+
+@pytest.mark.parametrize("name", ["qmv_moe_grouped", "qmv_moe_grouped_swiglu"])
+def test_a_plan_read_on_another_stream_is_kept_for_it(stand, name):
+    st, qmv = stand
+    f = getattr(qmv, name)
+
+    def product(plan, s):
+        f("q4_0", raw(8 * MOE[0]), *MOE, plan, 2, gpu(3, 64), stream=s)
+    plan = qmv.qmv_group_plan(ids(3, 2), 4)
+    product(plan, None)
+    assert not hasattr(plan.buffer, "recorded")
+    product(plan, st.side)
+    assert plan.buffer.recorded == [st.side]
+    plan = qmv.qmv_group_plan(ids(3, 2), 4, stream=st.side)
+    before = list(plan.buffer.recorded)
+    product(plan, st.side)
+    assert plan.buffer.recorded == before
+    product(plan, None)
+    assert plan.buffer.recorded == before + [st.main]
+    given = raw(64)
+    plan = qmv.qmv_group_plan(ids(3, 2), 4, plan=given)      # whose pool it is from is not known
+    product(plan, None)
+    assert given.recorded == [st.main]
