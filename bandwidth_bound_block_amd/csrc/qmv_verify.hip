@@ -56,25 +56,29 @@ struct VerifyArgs {
 
 __device__ __forceinline__ int drafts_of(const VerifyArgs& a, int r) { return min(max(a.n_draft[r], 0), a.D); }
 
-// e^x for x <= 0 to about 7e-12: x = n ln 2 + f, |f| <= ln 2 / 2, the Taylor
-// polynomial of degree 9 (its remainder f^10 / 10!), times 2^n; over 1.5e5
-// tokens that leaves a draw off the exact one about once in 1e6.  Below -700
-// the value is 0 beside a row's largest term, 1; NaN stays NaN.
+// e^x for x <= 0 to 5e-14: x = n ln 2 + f, |f| <= ln 2 / 2 (the rounding of
+// ln 2 adds n 2.3e-17), e^f by the Taylor polynomial of degree 20 economized
+// to degree 9 (its terms past that in Chebyshev polynomials of f / (ln 2 / 2)
+// dropped: 1.9e-14 of e^f), times 2^n.  The Taylor polynomial of degree 9
+// itself costs the same and is up to 7e-12 off, always one way; degree 10
+// and ln 2 in two parts (1e-15) take the largest batch from 79 to 83 us.
+// Below -746 the value is less than half of the smallest number; NaN stays
+// NaN.
 __device__ __forceinline__ double exp_neg(double x) {
     const double n = __builtin_rint(x * 1.4426950408889634074);
     const double f = __builtin_fma(n, -0x1.62e42fefa39efp-1, x);
-    double p = 1.0 / 362880.0;
-    p = __builtin_fma(p, f, 1.0 / 40320.0);
-    p = __builtin_fma(p, f, 1.0 / 5040.0);
-    p = __builtin_fma(p, f, 1.0 / 720.0);
-    p = __builtin_fma(p, f, 1.0 / 120.0);
-    p = __builtin_fma(p, f, 1.0 / 24.0);
-    p = __builtin_fma(p, f, 1.0 / 6.0);
-    p = __builtin_fma(p, f, 0.5);
-    p = __builtin_fma(p, f, 1.0);
-    p = __builtin_fma(p, f, 1.0);
+    double p = 0x1.72faf16b7bd05p-19;
+    p = __builtin_fma(p, f, 0x1.a17df2ec2bc60p-16);
+    p = __builtin_fma(p, f, 0x1.a01978c559bacp-13);
+    p = __builtin_fma(p, f, 0x1.6c162bb5db14bp-10);
+    p = __builtin_fma(p, f, 0x1.1111112dd6fbap-7);
+    p = __builtin_fma(p, f, 0x1.55555588b972bp-5);
+    p = __builtin_fma(p, f, 0x1.555555554b752p-3);
+    p = __builtin_fma(p, f, 0x1.ffffffffe74e3p-2);
+    p = __builtin_fma(p, f, 0x1.000000000001ep+0);
+    p = __builtin_fma(p, f, 0x1.000000000003dp+0);
     p = __builtin_ldexp(p, (int)n);
-    return x < -700.0 ? 0.0 : p;
+    return x < -746.0 ? 0.0 : p;
 }
 
 __device__ __forceinline__ double wave_sum(double s) {

@@ -576,7 +576,10 @@ int32_t qmv_lora(qmv_fmt fmt, const void* W, int64_t n_rows, int64_t n_cols, con
  *   n_requests 1..65535, max_drafts 1..64, vocab 1..2^22.
  *   workspace  device memory of >= qmv_spec_verify_workspace_bytes(...)
  *              bytes, 16-byte aligned; any contents.
- * Exponentials and sums are fp64.  Errors: QMV_EINVAL, QMV_EALIGN, QMV_EHIP.
+ * Exponentials and sums are fp64, the exponentials to 5e-14; a logit more
+ * than 745 below its row's largest, whose exponential is no fp64 number, is a
+ * probability of 0.
+ * Errors: QMV_EINVAL, QMV_EALIGN, QMV_EHIP.
  */
 size_t qmv_spec_verify_workspace_bytes(int64_t n_requests, int32_t max_drafts, int64_t vocab);
 int32_t qmv_spec_verify(const void* logits, int32_t logits_type, int64_t logits_stride_request,
