@@ -575,7 +575,8 @@ int32_t qmv_lora(qmv_fmt fmt, const void* W, int64_t n_rows, int64_t n_cols, con
  *   n_kept     int32 [n_requests].
  *   n_requests 1..65535, max_drafts 1..64, vocab 1..2^22.
  *   workspace  device memory of >= qmv_spec_verify_workspace_bytes(...)
- *              bytes, 16-byte aligned; any contents.
+ *              bytes, 16-byte aligned; any contents; calls that share one must
+ *              not run concurrently (values pass between launches in it).
  * Exponentials and sums are fp64, the exponentials to 5e-14; a logit more
  * than 745 below its row's largest, whose exponential is no fp64 number, is a
  * probability of 0.
