@@ -1102,7 +1102,8 @@ int32_t launch_tile(const TileCall& c, int plan_tile, hipStream_t st) {
         grid = whole * d.row_tiles;
     else
         grid = (whole * units + kXcds - 1) / kXcds * kXcds * split * d.row_unit;
-    if (grid > 0x7fffffff) return fail(QMV_EINVAL, "qmv: %lld tiles exceed a launch", (long long)grid);
+    if (grid > 0xffffffffll / S::kThreads)        // a launch's threads are counted in 32 bits
+        return fail(QMV_EINVAL, "qmv: %lld tiles exceed a launch", (long long)grid);
     auto kern = tile_kernel<F, XT, TN, KG, LORA>;
     size_t dyn_max = 0;
     if (const int32_t e = lds_limit(reinterpret_cast<const void*>(kern), kLdsMax, "qmv", &dyn_max)) return e;
