@@ -499,7 +499,7 @@ int32_t qmv_group_plan(const int32_t* group_ids, int64_t n_items, int32_t n_grou
  * outputs do not depend on the other items' values; how many items there are
  * can change the order of the fp32 sums.
  * A launch holds 2^32 threads: a call whose (n_tokens * top_k / 32 + n_experts
- * + 1) * n_rows / 128 (n_ff / 64) passes 2^24 may be refused (QMV_EINVAL).
+ * + 1) * n_rows / 128 (n_ff / 64) passes 2^23 may be refused (QMV_EINVAL).
  * Errors: QMV_EINVAL, QMV_EALIGN, QMV_EUNSUPPORTED (unknown fmt), QMV_EHIP.
  */
 int32_t qmv_moe_grouped(qmv_fmt fmt, const void* W_experts, int64_t expert_stride_bytes, int32_t n_experts,
