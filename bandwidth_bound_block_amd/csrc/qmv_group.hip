@@ -172,7 +172,8 @@ __global__ __launch_bounds__(kPlanThreads) void plan_kernel(const int32_t* __res
 }
 
 // out[t][n] = sum_s w[t][s] y[t][s][n], an fp32 fused multiply-add chain in
-// slot order; four columns a thread.
+// slot order; four columns a thread, in turns where a launch's threads (2^32)
+// do not reach.
 template <class YT>
 __device__ __forceinline__ float4 y4(const YT* p, int left, bool vec) {
     if (vec) return XIn<YT>::load4(p);
@@ -189,26 +190,25 @@ template <class YT, class OT>
 __global__ __launch_bounds__(256) void weighted_sum_kernel(const YT* __restrict__ y, const float* __restrict__ w,
                                                            int64_t tokens, int top_k, int64_t n, int64_t quads,
                                                            OT* __restrict__ out, int vec) {
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (i >= tokens * quads) return;
-    const int64_t t = i / quads, c = 4 * (i - t * quads);
-    const int left = (int)min((int64_t)4, n - c);
-    float a[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int s = 0; s < top_k; ++s) {
-        const float4 v = y4<YT>(y + (t * top_k + s) * n + c, left, vec);
-        const float f = w[t * top_k + s];
-        a[0] = __builtin_fmaf(f, v.x, a[0]);
-        a[1] = __builtin_fmaf(f, v.y, a[1]);
-        a[2] = __builtin_fmaf(f, v.z, a[2]);
-        a[3] = __builtin_fmaf(f, v.w, a[3]);
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < tokens * quads; i += (int64_t)gridDim.x * 256) {
+        const int64_t t = i / quads, c = 4 * (i - t * quads);
+        const int left = (int)min((int64_t)4, n - c);
+        float a[4] = {0.f, 0.f, 0.f, 0.f};
+        for (int s = 0; s < top_k; ++s) {
+            const float4 v = y4<YT>(y + (t * top_k + s) * n + c, left, vec);
+            const float f = w[t * top_k + s];
+            a[0] = __builtin_fmaf(f, v.x, a[0]);
+            a[1] = __builtin_fmaf(f, v.y, a[1]);
+            a[2] = __builtin_fmaf(f, v.z, a[2]);
+            a[3] = __builtin_fmaf(f, v.w, a[3]);
+        }
+        for (int k = 0; k < left; ++k) out[t * n + c + k] = narrow<OT>(a[k]);
     }
-    for (int k = 0; k < left; ++k) out[t * n + c + k] = narrow<OT>(a[k]);
 }
 
 template <class YT>
 int32_t launch_sum(const YT* y, const float* w, int64_t T, int S, int64_t n, void* out, int32_t ot, hipStream_t st) {
-    const int64_t quads = (n + 3) / 4, blocks = (T * quads + 255) / 256;
-    if (blocks > 0x7fffffff) return fail(QMV_EINVAL, "qmv_moe_weighted_sum: too many outputs for a launch");
+    const int64_t quads = (n + 3) / 4, blocks = std::min<int64_t>((T * quads + 255) / 256, 0xffffffff / 256);
     const int vec = n % 4 == 0 && aligned(y, XIn<YT>::kVecAlign);
     const dim3 g((unsigned)blocks), b(256);
     switch (ot) {
