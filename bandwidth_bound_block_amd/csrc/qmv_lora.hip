@@ -48,6 +48,16 @@ template <bool F16> struct Piece<float, F16> {
     __device__ static void of(const X8<float>& x, u32x4 (&p)[3]) { x.pieces(p); }
 };
 
+// The sum of x[k] a[k] over a part's columns: 512 of every 512 * parts.
+template <class XT, class AT>
+__device__ __forceinline__ float part_sum(const XT* x, const AT* a, int64_t K, int part, int parts) {
+    float s = 0.f;
+    for (int64_t c0 = 512 * part; c0 < K; c0 += 512 * parts)
+#pragma unroll 8
+        for (int64_t c = c0; c < min(c0 + 512, K); ++c) s = __builtin_fmaf(XIn<XT>::load1(x + c), XIn<AT>::load1(a + c), s);
+    return s;
+}
+
 // v[part][t][r] = scales[a] * sum over the part's columns of A[a][r][k] x[t][k].
 // A workgroup takes 32 tokens and a part of the columns; its four waves take
 // groups of 128 columns in turn, and the sums of an adapter's rows with all
@@ -123,9 +133,12 @@ __global__ __launch_bounds__(256) void lora_shrink_kernel(const XT* __restrict__
         const float sc = scales[ad];
         for (int i = tid; i < 32 * rank; i += 256) {
             const int j = i / rank, r = i % rank;
-            if (own >> j & 1)
-                v[((int64_t)part * T + t0 + j) * rank + r] =
-                    sc * ((red[0][j][r] + red[1][j][r]) + (red[2][j][r] + red[3][j][r]));
+            if (!(own >> j & 1)) continue;
+            float s = (red[0][j][r] + red[1][j][r]) + (red[2][j][r] + red[3][j][r]);
+            // an infinity's pieces are NaN: its products one by one
+            if (!(__builtin_fabsf(s) < __builtin_inff()))
+                s = part_sum<XT, AT>(x + (int64_t)(t0 + j) * ldx, A + ((int64_t)ad * rank + r) * K, K, part, parts);
+            v[((int64_t)part * T + t0 + j) * rank + r] = sc * s;
         }
     }
 }

@@ -100,6 +100,7 @@ template <> struct XOp<_Float16> {
 // at(h, lh) .. + 7, as signed bytes.
 //   kRow    bytes of eight blocks;  kCpr  pieces of a row;  kPitch  bytes of
 //   a slot's row, an odd number of 16-byte units.
+// weight() is the weight of column c of the row at `row` in memory, in fp32.
 template <class F> struct Unit;
 
 __device__ __forceinline__ uint32_t lds4(const uint8_t* p) { return *reinterpret_cast<const uint32_t*>(p); }
@@ -145,6 +146,10 @@ __device__ __forceinline__ float pivot(float D, float M) {
 template <> struct Unit<Q8_0> {
     static constexpr int kSub = 1, kRow = 272, kCpr = 18, kPitch = 304;
     static constexpr bool kSums = false;
+    __device__ static float weight(const uint8_t* row, int c) {
+        const uint8_t* blk = row + 34 * (c >> 5);
+        return half_bits_to_float(ld2(blk)) * (float)(int8_t)blk[2 + (c & 31)];
+    }
     __device__ static constexpr int at(int h, int lh) { return 16 * lh + 8 * h; }
     struct Raw {
         uint32_t w[2][5];
@@ -174,6 +179,10 @@ template <> struct Unit<Q8_0> {
 template <> struct Unit<Q4_0> {
     static constexpr int kSub = 1, kRow = 144, kCpr = 10, kPitch = 176;
     static constexpr bool kSums = false;
+    __device__ static float weight(const uint8_t* row, int c) {
+        const uint8_t* blk = row + 18 * (c >> 5);
+        return half_bits_to_float(ld2(blk)) * (float)((blk[2 + (c & 15)] >> (c & 16 ? 4 : 0) & 15) - 8);
+    }
     __device__ static constexpr int at(int h, int lh) { return 16 * h + 8 * lh; }
     struct Raw {
         uint32_t w[2][3];
@@ -207,6 +216,11 @@ template <> struct Unit<Q4_0> {
 template <> struct Unit<Q4_1> {
     static constexpr int kSub = 1, kRow = 160, kCpr = 10, kPitch = 176;
     static constexpr bool kSums = true;
+    __device__ static float weight(const uint8_t* row, int c) {
+        const uint8_t* blk = row + 20 * (c >> 5);
+        return __builtin_fmaf(half_bits_to_float(ld2(blk)), (float)(blk[4 + (c & 15)] >> (c & 16 ? 4 : 0) & 15),
+                              half_bits_to_float(ld2(blk + 2)));
+    }
     __device__ static constexpr int at(int h, int lh) { return 16 * h + 8 * lh; }
     struct Raw {
         uint32_t w[2][2], dm;
@@ -239,6 +253,16 @@ struct Q4KTile {};
 template <> struct Unit<Q4KTile> {
     static constexpr int kSub = 1, kRow = 144, kCpr = 9, kPitch = 144;
     static constexpr bool kSums = true;
+    __device__ static float weight(const uint8_t* row, int c) {
+        const uint8_t* sb = row + 144 * (c >> 8);
+        const int b = c >> 5 & 7, k = b & 3;
+        const uint32_t f1 = sb[4 + k], f2 = sb[8 + k], f3 = sb[12 + k];
+        const uint32_t sc = b < 4 ? f1 & 63u : (f3 & 15u) | (f1 >> 2 & 48u);
+        const uint32_t mn = b < 4 ? f2 & 63u : (f3 >> 4) | (f2 >> 2 & 48u);
+        const uint32_t q = sb[16 + 32 * (b >> 1) + (c & 31)] >> (b & 1 ? 4 : 0) & 15;
+        return __builtin_fmaf(half_bits_to_float(ld2(sb)) * (float)sc, (float)q,
+                              -(half_bits_to_float(ld2(sb + 2)) * (float)mn));
+    }
     __device__ static constexpr int at(int h, int lh) { return 16 * lh + 8 * h; }
     struct Raw {
         u32x4 head, c;
@@ -272,6 +296,13 @@ struct Q6KTile {};
 template <> struct Unit<Q6KTile> {
     static constexpr int kSub = 2, kRow = 210, kCpr = 14, kPitch = 240;
     static constexpr bool kSums = false;
+    __device__ static float weight(const uint8_t* row, int c) {
+        const uint8_t* sb = row + 210 * (c >> 8);
+        const int h = c >> 7 & 1, q = c >> 5 & 3, l = c & 31;       // half of the super-block, its quarter
+        const uint32_t lo = sb[64 * h + 32 * (q & 1) + l] >> (q & 2 ? 4 : 0) & 15;
+        const uint32_t hi = sb[128 + 32 * h + l] >> (2 * q) & 3;
+        return half_bits_to_float(ld2(sb + 208)) * (float)(int8_t)sb[192 + (c >> 4 & 15)] * (float)((int)(lo | hi << 4) - 32);
+    }
     __device__ static constexpr int at(int h, int lh) { return 16 * h + 8 * lh; }     // an MFMA is one scale's 16 weights
     struct Raw {
         uint32_t lo[2][2][3], hi[2][3], sc[2];     // [b][h], [h]
@@ -438,6 +469,31 @@ __device__ __forceinline__ void store_y4(void* y, int y_type, int64_t at, f32x4 
     *reinterpret_cast<uint2*>(static_cast<uint16_t*>(y) + at) = uint2{w[0], w[1]};
 }
 
+// The kernel's arguments and the lane's number, read at this place.
+__device__ __forceinline__ const TileDev& again_args() {
+    auto p = reinterpret_cast<uintptr_t>(__builtin_amdgcn_kernarg_segment_ptr());
+    asm volatile("" : "+s"(p));
+    return *reinterpret_cast<const TileDev*>(p);
+}
+__device__ __forceinline__ int again_lane() {
+    int all = -1;
+    asm volatile("" : "+s"(all));
+    return (int)__builtin_amdgcn_mbcnt_hi(all, __builtin_amdgcn_mbcnt_lo(all, 0));
+}
+
+__device__ __forceinline__ bool finite(f32x4 v) {
+    const float inf = __builtin_inff();
+    return __builtin_fabsf(v[0]) < inf && __builtin_fabsf(v[1]) < inf && __builtin_fabsf(v[2]) < inf &&
+           __builtin_fabsf(v[3]) < inf;
+}
+
+// An element of B.
+__device__ __forceinline__ float lora_b(const LoraTile& l, int64_t at) {
+    return l.b_type == QMV_X_F32   ? static_cast<const float*>(l.B)[at]
+           : l.b_type == QMV_X_F16 ? (float)static_cast<const _Float16*>(l.B)[at]
+                                   : (float)static_cast<const __bf16*>(l.B)[at];
+}
+
 constexpr int kLoraRanks = 64;                       // ranks staged at a time
 constexpr int kLoraPitch = 2 * kLoraRanks + 16;      // bytes of a token's piece, an odd number of 16-byte units
 
@@ -555,10 +611,7 @@ __device__ __forceinline__ void add_adapters(const LoraTile& l, const int* s_ada
                     const int r0 = 16 * s + 8 * lh;
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        const int64_t at = brow + min(r0 + i, ranks - 1);
-                        const float f = l.b_type == QMV_X_F32   ? static_cast<const float*>(l.B)[at]
-                                        : l.b_type == QMV_X_F16 ? (float)static_cast<const _Float16*>(l.B)[at]
-                                                                : (float)static_cast<const __bf16*>(l.B)[at];
+                        const float f = lora_b(l, brow + min(r0 + i, ranks - 1));
                         b.v[i] = r0 + i < ranks ? f : 0.f;
                     }
                 }
@@ -659,7 +712,7 @@ __global__ __launch_bounds__((TileShape<F, XT, TN, KG>::kThreads), (TileShape<F,
     using S = TileShape<F, XT, TN, KG>;
     using U = Unit<F>;
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
-    __shared__ int s_item[TN], s_adapter[LORA ? TN : 1];
+    __shared__ int s_item[TN], s_adapter[LORA ? TN : 1], s_group;
     __shared__ int64_t s_x[TN];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -761,6 +814,7 @@ __global__ __launch_bounds__((TileShape<F, XT, TN, KG>::kThreads), (TileShape<F,
     };
     load_w(0);
 
+    if (tid == 0) s_group = group;
     if (tid < TN) {
         const int at = start + min(tid, count - 1);
         const int item = a.plan ? a.plan[a.order_at + at] : at;
@@ -1043,24 +1097,91 @@ __global__ __launch_bounds__((TileShape<F, XT, TN, KG>::kThreads), (TileShape<F,
     __syncthreads();
     // four rows a thread; rows of a tile are a power of two
     const int quads = out_rows >> 2, qshift = __builtin_ctz(quads);
-    for (int i = tid; i < count << qshift; i += S::kThreads) {
+    const int all_quads = count << qshift;
+    auto result = [&](int j, int rr) __attribute__((always_inline)) {
+        f32x4 v = *reinterpret_cast<const f32x4*>(out + j * S::kOutPitch + rr);
+#pragma unroll
+        for (int k = 1; k < KG; ++k) v += *reinterpret_cast<const f32x4*>(out + (k * TN + j) * S::kOutPitch + rr);
+        return v;
+    };
+    float open = 0.f;             // NaN once an output of this thread's is not finite
+    for (int i = tid; i < all_quads; i += S::kThreads) {
         const int j = i >> qshift, r = (i & (quads - 1)) << 2;
-        auto result = [&](int rr) __attribute__((always_inline)) {
-            f32x4 v = *reinterpret_cast<const f32x4*>(out + j * S::kOutPitch + rr);
-#pragma unroll
-            for (int k = 1; k < KG; ++k) v += *reinterpret_cast<const f32x4*>(out + (k * TN + j) * S::kOutPitch + rr);
-            return v;
-        };
-        f32x4 v = result(r);
+        f32x4 v = result(j, r);
         if (a.swiglu) {
-            const f32x4 u = result(out_rows + r);
+            const f32x4 u = result(j, out_rows + r);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) v[k] = silu(v[k]) * u[k];
+            for (int k = 0; k < 4; ++k) v[k] = silu(v[k]) * u[k];      // of a sum that is not finite: not finite
         }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) open = __builtin_fmaf(v[k], 0.f, open);
         if constexpr (LORA) {
             if (s_adapter[j] < -1 || s_adapter[j] >= a.lora.n_adapters) v = f32x4{1.f, 1.f, 1.f, 1.f} * __builtin_nanf("");
         }
         store_y4(a.y, a.y_type, (int64_t)s_item[j] * a.ldy + row0 + r, v, a.rows - row0 - r, a.yvec != 0);
+    }
+    if (__ballot(open != 0.f) == 0) return;
+
+    // Sums that are not finite.  An infinite activation (and a finite one
+    // that the first bf16 piece or a block's sum of codes takes past the
+    // largest float) meets zero codes, pieces of NaN and both terms of a
+    // minimum: NaN where the weights' own products give an infinity, or a
+    // number.  These outputs are computed again from the weights one by one,
+    // by the whole wave.  A token with a NaN keeps its NaN.  What this needs
+    // of the arguments and the lane's number is read again: held through the
+    // main loop it took four registers.  Where all sums are finite the test
+    // for it costs up to 1% (block of 2048 tokens 485.3 -> 489 us, 101 tokens
+    // with 40 adapters 96.9 -> 98.2).
+    const TileDev& b = again_args();
+    const int l64 = again_lane();
+    const uint8_t* wmat = b.W + min(s_group, b.n_groups - 1) * b.estride;
+    const int64_t row_bytes = (int64_t)(b.nb / 8 * U::kRow + b.nb % 8 * (U::kRow / 8));
+    int looked = -1;              // the token looked through last, whether it holds a NaN
+    bool nan_in = false;
+    for (int i0 = 64 * wave; i0 < all_quads; i0 += S::kThreads) {
+        const int i = min(i0 + l64, all_quads - 1), j = i >> qshift, r = (i & (quads - 1)) << 2;
+        bool again = !finite(result(j, r));
+        if (b.swiglu) again |= !finite(result(j, out_rows + r));
+        if constexpr (LORA) again &= s_adapter[j] >= -1 && s_adapter[j] < b.lora.n_adapters;
+        for (uint64_t todo = __ballot(again && i0 + l64 < all_quads); todo; todo &= todo - 1) {
+            const int from = __builtin_ctzll(todo);
+            const int jj = __builtin_amdgcn_readlane(j, from), rr = row0 + __builtin_amdgcn_readlane(r, from);
+            const XT* x = static_cast<const XT*>(b.x) + s_x[jj];
+            if (looked != jj) {
+                looked = jj;
+                bool n = false;
+                for (int c = l64; c < 32 * b.nb; c += 64) {
+                    const float f = XIn<XT>::load1(x + c);
+                    n |= f != f;
+                }
+                nan_in = __ballot(n) != 0;
+            }
+            if (nan_in) continue;
+            for (int row = rr; row < min(rr + 4, b.rows); ++row) {
+                float v = 0.f;
+                for (int up = 0; up < (b.swiglu ? 2 : 1); ++up) {
+                    const uint8_t* wr = wmat + (up ? b.rows + row : row) * row_bytes;
+                    float s = 0.f;
+                    for (int blk = l64; blk < b.nb; blk += 64)
+#pragma unroll 8
+                        for (int c = 32 * blk; c < 32 * blk + 32; ++c)
+                            s = __builtin_fmaf(U::weight(wr, c), XIn<XT>::load1(x + c), s);
+                    if constexpr (LORA) {
+                        const int ad = s_adapter[jj];
+                        for (int k = l64; ad >= 0 && k < b.lora.rank; k += 64) {
+                            float t = 0.f;
+                            for (int p = 0; p < b.lora.parts; ++p)
+                                t += b.lora.v[((int64_t)p * b.n_items + s_item[jj]) * b.lora.rank + k];
+                            s = __builtin_fmaf(lora_b(b.lora, ((int64_t)ad * b.rows + row) * b.lora.rank + k), t, s);
+                        }
+                    }
+#pragma unroll
+                    for (int o = 32; o; o >>= 1) s += __shfl_xor(s, o);
+                    v = up ? silu(v) * s : s;
+                }
+                if (l64 == 0) store_y(b.y, b.y_type, (int64_t)s_item[jj] * b.ldy + row, v);
+            }
+        }
     }
 }
 

@@ -498,6 +498,9 @@ int32_t qmv_group_plan(const int32_t* group_ids, int64_t n_items, int32_t n_grou
  * scales are fp32: the accuracy contract holds as for the matvec.  An item's
  * outputs do not depend on the other items' values; how many items there are
  * can change the order of the fp32 sums.
+ * Activations outside the contract (infinities, |x| >= 8e34): a sum is that of
+ * the fp32 weights' own products, an infinity, NaN (0 times an infinity,
+ * infinities of both signs) or a number, as IEEE arithmetic gives it.
  * A launch holds 2^32 threads: a call whose (n_tokens * top_k / 32 + n_experts
  * + 1) * n_rows / 128 (n_ff / 64) passes 2^23 may be refused (QMV_EINVAL).
  * Errors: QMV_EINVAL, QMV_EALIGN, QMV_EUNSUPPORTED (unknown fmt), QMV_EHIP.
@@ -543,7 +546,9 @@ int32_t qmv_moe_weighted_sum(const void* y, int32_t y_type, const float* weights
  *            16-byte aligned; any contents; calls that share one must not
  *            run concurrently.
  * The base is the matvec's result up to 8 tokens (fp32 x: the FMA kernels',
- * QMV_PATH_FMA); the adapters' products and sums are fp32.  The same call
+ * QMV_PATH_FMA); the adapters' products and sums are fp32.  Activations
+ * outside the contract as in qmv_moe_grouped; up to 8 tokens the base's sums
+ * are the matvec's, which holds for finite ones.  The same call
  * gives the same bits; the other tokens' number and adapters can change the
  * order of a token's fp32 sums, nothing else.
  * Errors: QMV_EINVAL, QMV_EALIGN, QMV_EUNSUPPORTED (unknown fmt), QMV_EHIP.
