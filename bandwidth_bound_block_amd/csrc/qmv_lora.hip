@@ -143,16 +143,29 @@ __global__ __launch_bounds__(256) void lora_shrink_kernel(const XT* __restrict__
     }
 }
 
-// y[t][n] += sum_r B[a][n][r] v[t][r]; NaN for an id that is no adapter.
-template <class AT>
+// Sum of a row's weights times x, one by one.
+template <class F, class XT>
+__device__ float row_sum(const uint8_t* W, int64_t n, int nb, const XT* x) {
+    const uint8_t* row = W + n * (int64_t)(nb / 8 * Unit<F>::kRow + nb % 8 * (Unit<F>::kRow / 8));
+    float s = 0.f;
+    for (int b = 0; b < nb && s == s; ++b)
+#pragma unroll 8
+        for (int c = 32 * b; c < 32 * b + 32; ++c) s = __builtin_fmaf(Unit<F>::weight(row, c), XIn<XT>::load1(x + c), s);
+    return s;
+}
+
+// y[t][n] += sum_r B[a][n][r] v[t][r]; NaN for an id that is no adapter.  A
+// base sum that is not finite (an infinite activation's pieces are NaN in the
+// matrix-core matvec) is computed again first.
+template <class F, class AT>
 __global__ __launch_bounds__(256) void lora_expand_kernel(const AT* __restrict__ B, const int32_t* __restrict__ ids,
                                                           int n_adapters, int rank, int parts, int T, int N, int vec,
                                                           const float* __restrict__ v, float* __restrict__ y,
-                                                          int64_t ldy) {
+                                                          int64_t ldy, const uint8_t* __restrict__ W, int nb,
+                                                          const void* __restrict__ x, int x_type, int64_t ldx) {
     __shared__ float sv[128];
     const int t = blockIdx.x, n = blockIdx.y * 256 + threadIdx.x;
     const int a = ids[t];
-    if (a == -1) return;
     const bool good = (unsigned)a < (unsigned)n_adapters;
     if (good && (int)threadIdx.x < rank) {
         float s = 0.f;
@@ -162,28 +175,38 @@ __global__ __launch_bounds__(256) void lora_expand_kernel(const AT* __restrict__
     __syncthreads();
     if (n >= N) return;
     float* o = y + t * ldy + n;
-    if (!good) {
+    if (!good && a != -1) {
         *o = __builtin_nanf("");
         return;
     }
-    const AT* b = B + ((int64_t)a * N + n) * rank;
     float s = 0.f;
-    if (vec) {
-        for (int r = 0; r < rank; r += 4) {
-            const float4 w = XIn<AT>::load4(b + r);
-            s = __builtin_fmaf(w.x, sv[r], s);
-            s = __builtin_fmaf(w.y, sv[r + 1], s);
-            s = __builtin_fmaf(w.z, sv[r + 2], s);
-            s = __builtin_fmaf(w.w, sv[r + 3], s);
+    if (good) {
+        const AT* b = B + ((int64_t)a * N + n) * rank;
+        if (vec) {
+            for (int r = 0; r < rank; r += 4) {
+                const float4 w = XIn<AT>::load4(b + r);
+                s = __builtin_fmaf(w.x, sv[r], s);
+                s = __builtin_fmaf(w.y, sv[r + 1], s);
+                s = __builtin_fmaf(w.z, sv[r + 2], s);
+                s = __builtin_fmaf(w.w, sv[r + 3], s);
+            }
+        } else {
+            for (int r = 0; r < rank; ++r) s = __builtin_fmaf(XIn<AT>::load1(b + r), sv[r], s);
         }
-    } else {
-        for (int r = 0; r < rank; ++r) s = __builtin_fmaf(XIn<AT>::load1(b + r), sv[r], s);
     }
-    *o += s;
+    float base = *o;
+    if (!(__builtin_fabsf(base) < __builtin_inff())) {
+        base = x_type == QMV_X_F32   ? row_sum<F, float>(W, n, nb, static_cast<const float*>(x) + t * ldx)
+               : x_type == QMV_X_F16 ? row_sum<F, _Float16>(W, n, nb, static_cast<const _Float16*>(x) + t * ldx)
+                                     : row_sum<F, __bf16>(W, n, nb, static_cast<const __bf16*>(x) + t * ldx);
+    } else if (a == -1) {
+        return;
+    }
+    *o = base + s;
 }
 
 struct LoraCall {
-    const void* x;
+    const void *W, *x;
     int32_t x_type;
     int64_t ldx, T, N, K;
     const void *A, *B;
@@ -228,12 +251,23 @@ int32_t shrink_x(const LoraCall& c, hipStream_t st) {
     default: return shrink_r<__bf16, AT>(c, st);
     }
 }
-template <class AT>
-int32_t expand(const LoraCall& c, hipStream_t st) {
+template <class F, class AT>
+int32_t expand_f(const LoraCall& c, hipStream_t st) {
     const int vec = c.rank % 4 == 0 && aligned(c.B, XIn<AT>::kVecAlign);
-    hipLaunchKernelGGL((lora_expand_kernel<AT>), dim3((unsigned)c.T, (unsigned)((c.N + 255) / 256)), dim3(256), 0, st,
-                       (const AT*)c.B, c.ids, c.n_adapters, c.rank, c.parts, (int)c.T, (int)c.N, vec, c.v, c.y, c.ldy);
+    hipLaunchKernelGGL((lora_expand_kernel<F, AT>), dim3((unsigned)c.T, (unsigned)((c.N + 255) / 256)), dim3(256), 0, st,
+                       (const AT*)c.B, c.ids, c.n_adapters, c.rank, c.parts, (int)c.T, (int)c.N, vec, c.v, c.y, c.ldy,
+                       (const uint8_t*)c.W, (int)(c.K / 32), c.x, c.x_type, c.ldx);
     return check_launch("qmv_lora");
+}
+template <class AT>
+int32_t expand(qmv_fmt fmt, const LoraCall& c, hipStream_t st) {
+    switch (fmt) {
+    case QMV_Q8_0: return expand_f<Q8_0, AT>(c, st);
+    case QMV_Q4_0: return expand_f<Q4_0, AT>(c, st);
+    case QMV_Q4_1: return expand_f<Q4_1, AT>(c, st);
+    case QMV_Q4_K: return expand_f<Q4KTile, AT>(c, st);
+    default: return expand_f<Q6KTile, AT>(c, st);
+    }
 }
 
 constexpr int64_t kLoraTokens = 1 << 20;
@@ -279,7 +313,7 @@ extern "C" int32_t qmv_lora(qmv_fmt fmt, const void* W, int64_t n_rows, int64_t 
         !aligned(scales, 4) || !aligned(adapter_ids, 4) || !aligned(y, 4) || !aligned(workspace, 16))
         return fail(QMV_EALIGN, "%s: a pointer is not aligned to its elements (workspace: 16 bytes)", name);
     const hipStream_t st = as_stream(stream);
-    LoraCall c{x, x_type, ldx, n_tokens, n_rows, n_cols, A, B, a_type, n_adapters, rank, lora_parts(n_tokens, n_cols),
+    LoraCall c{W, x, x_type, ldx, n_tokens, n_rows, n_cols, A, B, a_type, n_adapters, rank, lora_parts(n_tokens, n_cols),
                scales, adapter_ids, y, ldy, static_cast<float*>(workspace)};
     int32_t rc;
     switch (a_type) {
@@ -312,8 +346,8 @@ extern "C" int32_t qmv_lora(qmv_fmt fmt, const void* W, int64_t n_rows, int64_t 
                                  n_tokens > 1 ? ldy : n_rows, stream, x_type == QMV_X_F32 ? QMV_PATH_FMA : QMV_PATH_AUTO);
     if (rc != QMV_OK) return rc;
     switch (a_type) {
-    case QMV_X_F32: return expand<float>(c, st);
-    case QMV_X_F16: return expand<_Float16>(c, st);
-    default: return expand<__bf16>(c, st);
+    case QMV_X_F32: return expand<float>(fmt, c, st);
+    case QMV_X_F16: return expand<_Float16>(fmt, c, st);
+    default: return expand<__bf16>(fmt, c, st);
     }
 }

@@ -547,10 +547,9 @@ int32_t qmv_moe_weighted_sum(const void* y, int32_t y_type, const float* weights
  *            run concurrently.
  * The base is the matvec's result up to 8 tokens (fp32 x: the FMA kernels',
  * QMV_PATH_FMA); the adapters' products and sums are fp32.  Activations
- * outside the contract as in qmv_moe_grouped; up to 8 tokens the base's sums
- * are the matvec's, which holds for finite ones.  The same call
- * gives the same bits; the other tokens' number and adapters can change the
- * order of a token's fp32 sums, nothing else.
+ * outside the contract as in qmv_moe_grouped.  The same call gives the same
+ * bits; the other tokens' number and adapters can change the order of a
+ * token's fp32 sums, nothing else.
  * Errors: QMV_EINVAL, QMV_EALIGN, QMV_EUNSUPPORTED (unknown fmt), QMV_EHIP.
  */
 size_t qmv_lora_workspace_bytes(int64_t n_tokens, int32_t rank, int32_t n_adapters);

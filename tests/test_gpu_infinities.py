@@ -137,3 +137,31 @@ def test_adapters(env, fmt, x_name, a_name, T, N, blocks, R):
     got, large = got[:CHECKED], np.zeros(CHECKED, bool)
     large[[4, 7, 8]] = x_name != "f16"          # the adapters' sums of the largest floats pass fp32
     assert_same(got[~torch.from_numpy(large)], out[~large], bound[~large], fmt)
+
+
+@pytest.mark.parametrize("x_name,a_name", [("f32", "bf16"), ("f16", "f16"), ("f16", "bf16"), ("bf16", "bf16"), ("bf16", "f32")])
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("first,T", [(0, 8), (1, 8), (0, 1), (1, 2), (3, 4)])
+def test_adapters_on_few_tokens(env, fmt, x_name, a_name, first, T):
+    """The base is the matvec's, on its matrix cores at some of these sizes: 256-column rows of 16-byte aligned blocks."""
+    torch, qmv = env
+    N, K, R, G = 1100, 512, 8, 3
+    raw = wl.quant_weights(fmt, f"t/inf/few/{fmt}", N, K)
+    xt, x = activations(torch, 9, K, x_name, 5)
+    xt, x = xt[first:first + T], x[first:first + T]
+    g = np.random.default_rng(R)
+    At, A = ov.as_type(torch, g.standard_normal((G, R, K)) / np.sqrt(K), a_name)
+    Bt, B = ov.as_type(torch, g.standard_normal((G, N, R)), a_name)
+    scales = g.uniform(0.5, 2, size=G).astype(np.float32)
+    for ids in (np.full(T, -1), np.arange(T) % (G + 2) - 1):
+        y, _ = values(fmt, raw, N, K, x)
+        w = ov.oracle.dequant(fmt, raw, N, K).astype(np.float64).reshape(N, K)
+        with np.errstate(invalid="ignore", over="ignore"):
+            e = np.stack([1e-4 * np.abs(w * v).sum(1) + 1e-6 for v in x])       # the matvec's contract
+            d, ed = ov.adapters(x, A, B, scales, ids)
+            out, bound = y + d, e + ed + 2 * ov.U * (np.abs(y) + np.abs(d))
+        out[ids >= G] = np.nan
+        got = qmv.qmv_lora(fmt, torch.from_numpy(raw.reshape(-1)).cuda(), N, K, xt.cuda(), At.cuda(), Bt.cuda(),
+                           torch.from_numpy(scales).cuda(), torch.from_numpy(ids.astype(np.int32)).cuda())
+        keep = np.array([first + t not in (4, 7, 8) or x_name == "f16" or ids[t] == -1 for t in range(T)])
+        assert_same(got[torch.from_numpy(keep)], out[keep], bound[keep], (fmt, list(ids)))
