@@ -271,6 +271,8 @@ int32_t expand(qmv_fmt fmt, const LoraCall& c, hipStream_t st) {
 }
 
 constexpr int64_t kLoraTokens = 1 << 20;
+constexpr int64_t kMatvecTokens = 8, kMatvecCols = 35424;     // the base is the matvec, whose rows have to fit LDS
+constexpr int64_t kTileCols = 1 << 24;
 constexpr int kLoraRank = 128, kLoraAdapters = 1024;
 
 }  // namespace
@@ -282,7 +284,7 @@ extern "C" size_t qmv_lora_workspace_bytes(int64_t n_tokens, int32_t rank, int32
         n_adapters > kLoraAdapters)
         return 0;
     // v in at most as many parts as the longest rows have
-    return (size_t)n_tokens * rank * 4 * lora_parts(n_tokens, 35424);
+    return (size_t)n_tokens * rank * 4 * lora_parts(n_tokens, kTileCols);
 }
 
 extern "C" int32_t qmv_lora(qmv_fmt fmt, const void* W, int64_t n_rows, int64_t n_cols, const void* x, int32_t x_type,
@@ -297,9 +299,11 @@ extern "C" int32_t qmv_lora(qmv_fmt fmt, const void* W, int64_t n_rows, int64_t 
         return fail(QMV_EINVAL, "%s: null pointer", name);
     if (!x_type_ok(x_type) || !x_type_ok(a_type)) return fail(QMV_EINVAL, "%s: unknown element type", name);
     if (n_rows < 1 || n_rows > (1 << 24)) return fail(QMV_EINVAL, "%s: n_rows must be 1..2^24", name);
-    if (n_cols < uw || n_cols % uw || n_cols > 35424)
-        return fail(QMV_EINVAL, "%s: n_cols must be a multiple of %d in %d..35424", name, uw, uw);
     if (n_tokens < 1 || n_tokens > kLoraTokens) return fail(QMV_EINVAL, "%s: n_tokens must be 1..2^20", name);
+    const int64_t most_cols = n_tokens > kMatvecTokens ? kTileCols : kMatvecCols;
+    if (n_cols < uw || n_cols % uw || n_cols > most_cols)
+        return fail(QMV_EINVAL, "%s: n_cols must be a multiple of %d in %d..%lld for %lld tokens", name, uw, uw,
+                    (long long)most_cols, (long long)n_tokens);
     if (n_adapters < 1 || n_adapters > kLoraAdapters)
         return fail(QMV_EINVAL, "%s: n_adapters must be 1..%d", name, kLoraAdapters);
     if (rank < 1 || rank > kLoraRank) return fail(QMV_EINVAL, "%s: rank must be 1..%d", name, kLoraRank);
@@ -322,7 +326,7 @@ extern "C" int32_t qmv_lora(qmv_fmt fmt, const void* W, int64_t n_rows, int64_t 
     default: rc = shrink_x<__bf16>(c, st);
     }
     if (rc != QMV_OK) return rc;
-    if (n_tokens > 8) {
+    if (n_tokens > kMatvecTokens) {
         TileCall t{};
         t.W = static_cast<const uint8_t*>(W);
         t.rows = n_rows;

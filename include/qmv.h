@@ -537,7 +537,8 @@ int32_t qmv_moe_weighted_sum(const void* y, int32_t y_type, const float* weights
  * a = -1: the base alone.  Any other id outside [0, n_adapters): the token's
  * outputs are quiet NaN.
  *   W, n_rows, n_cols, x, x_type, ldx, y, ldy  as qmv_matvec_xt, with n_rows
- *            up to 2^24, n_cols up to 35424 and 1..2^20 tokens.
+ *            up to 2^24, n_cols up to 35424 (past 8 tokens 2^24) and 1..2^20
+ *            tokens.
  *   A        a_type (QMV_X_F32, QMV_X_F16, QMV_X_BF16) [n_adapters][rank][n_cols]
  *   B        a_type [n_adapters][n_rows][rank]
  *   rank     1..128 (smaller adapters padded with zeros);  n_adapters 1..1024.
