@@ -37,7 +37,7 @@ struct LoraTile {
     const int32_t* ids;
     const float* v;         // [parts][n_items][rank]
     int32_t b_type, n_adapters, rank, parts;
-    int32_t vec;            // rows of B may be read in 16-byte pieces
+    int32_t b16;            // 16-bit B whose rows may be read in 16-byte pieces of eight ranks
 };
 
 // One tiled product.  plan == nullptr: one matrix, the items are rows

@@ -274,8 +274,6 @@ int32_t grouped_entry(const char* name, bool swiglu, qmv_fmt fmt, const void* W,
     return tile_product(fmt, c, as_stream(stream));
 }
 
-}  // namespace
-
 int32_t make_plan(const char* name, const int32_t* ids, int64_t n, int32_t E, int32_t* plan, hipStream_t st) {
     const size_t lds = sizeof(int) * (size_t)(E + 1) * (kPlanWaves + 2);
     size_t dyn_max = 0;
@@ -287,6 +285,7 @@ int32_t make_plan(const char* name, const int32_t* ids, int64_t n, int32_t E, in
     return check_launch(name);
 }
 
+}  // namespace
 }  // namespace qmv
 
 extern "C" size_t qmv_group_plan_bytes(int64_t n_items, int32_t n_groups) {

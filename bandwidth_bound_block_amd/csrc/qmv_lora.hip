@@ -341,7 +341,7 @@ extern "C" int32_t qmv_lora(qmv_fmt fmt, const void* W, int64_t n_rows, int64_t 
         t.y_type = QMV_X_F32;
         t.ldy = ldy;
         t.lora = LoraTile{B, adapter_ids, c.v, a_type, n_adapters, rank, c.parts,
-                          rank % 8 == 0 && aligned(B, 16)};
+                          a_type != QMV_X_F32 && rank % 8 == 0 && aligned(B, 16)};
         return tile_product(fmt, t, st);
     }
     // fp32 activations by the FMA kernels: the matrix-core matvec holds them

@@ -575,9 +575,8 @@ __device__ __forceinline__ void add_adapters(const LoraTile& l, const int* s_ada
                 if (ad < 0 || turn++ % KG == wk) return ad;
             }
         };
-        const bool b16 = l.b_type != QMV_X_F32 && l.vec;      // rows of B in 16-byte pieces of eight ranks
         auto load_b = [&](int ad, u32x4 (&w)[kSteps]) __attribute__((always_inline)) {
-            if (!b16 || ad < 0) return;
+            if (!l.b16 || ad < 0) return;
             const uint16_t* b = static_cast<const uint16_t*>(l.B) + ((int64_t)ad * rows + row) * l.rank + c0;
 #pragma unroll
             for (int s = 0; s < kSteps; ++s) {
@@ -599,7 +598,7 @@ __device__ __forceinline__ void add_adapters(const LoraTile& l, const int* s_ada
             for (int s = 0; s < kSteps; ++s) {
                 if (s >= steps) continue;
                 X8<float> b;
-                if (b16) {
+                if (l.b16) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const bool half = l.b_type == QMV_X_F16;
