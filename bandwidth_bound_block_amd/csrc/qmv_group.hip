@@ -8,9 +8,15 @@
 
 namespace qmv {
 
-// 32 experts of 1536 x 2048, bf16, 32 / 48 / 64 tokens each: tiles of 32 take
-// 39 / 50 / 51 us (Q4_0) and 45 / 58 / 60 (Q4_K), tiles of 128 47 / 48 / 49
-// and 63 / 64 / 65.
+// One plan serves every product of its routing, of any format and activation
+// type; their borders lie apart, and 48 between them.  Routed at random, tiles
+// of 32 / of 128: 128 experts of 1536 x 2048, 48 and 64 tokens each on average,
+// bf16: Q4_0 122 / 129 and 149 / 137 us, Q8_0 191 / 169 and 223 / 175, Q4_K 156
+// / 177 and 184 / 183, Q6_K 193 / 268 and 247 / 272; fp32: Q4_0 404 / 193 and
+// 457 / 260.  8 experts of 4096 x 4096: Q4_0 46 / 64 and 56 / 65, Q8_0 54 / 72
+// and 86 / 74, Q6_K 75 / 117 and 98 / 118; fp32: Q4_0 125 / 72.  32 experts of
+// 1536 x 2048, 32 and 40 tokens each: Q4_0 34 / 43 and 32 / 44, Q8_0 50 / 51
+// and 52 / 52, Q6_K 51 / 80 and 53 / 81.
 int plan_tile(int64_t n_items, int n_groups) { return n_items >= 48 * (int64_t)n_groups ? 128 : 32; }
 
 bool fmt_unit(qmv_fmt fmt, int* weights, int* bytes) {

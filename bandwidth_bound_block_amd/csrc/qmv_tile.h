@@ -701,6 +701,9 @@ struct TileShape {
     static constexpr int kMain = 2 * kBuf + kWaves * kSlot;
     static constexpr int kLora = 3 * TN * kLoraPitch;
     static constexpr int kLds = kMain > kOut ? kMain : kOut;
+    // workgroups that a compute unit holds: by registers, and by LDS with what
+    // the kernel has of its own (under 1 KB at 32 tokens)
+    static constexpr int kWgs = std::min(4 * kOcc / kWaves, kLdsMax / (kLds + 1024));
     static_assert(kXL >= 1 && kCHS >= 1, "every thread stages, every wave computes");
 };
 
@@ -1240,19 +1243,31 @@ int32_t launch_tile_s(const TileCall& c, int tile, hipStream_t st) {
 
 // Which tile.  TN 128 by 128 rows (fp32 activations, of three times the LDS
 // and MFMAs: 64) where the plan's tiles are of 128 and one workgroup each
-// fills the GPU: 32 experts of 1536 x 2048 Q4_0, bf16, 64 / 96 / 128 tokens
-// each 49 / 52 / 85 us against 51 / 65 / 80 with TN 32.  Elsewhere TN 32:
-// 8 experts of 2048 x 4096, 16 / 48 / 96 tokens each 22 / 30 / 51 us.  There,
-// waves of a workgroup share rows (KG) where one per 32 rows and tile would
-// leave the GPU's SIMDs short of waves.  16-bit activations, at most a wave
-// per compute unit: KG 8 (9 tokens through 4096 x 14336: Q8_0 55 us against
-// 63 with KG 4, Q4_K 58 against 72; with 1.75 waves, 14336 x 4096 Q8_0, KG 4
-// 37 against 49); under one a SIMD: KG 4 (101 tokens through 4096 x 14336
-// Q4_K 262 / 257 us with KG 2 / 4, before the loads below); under two: KG 2
-// (352 with KG 1).  fp32, whose pieces take three times the LDS: at most a
-// wave per compute unit KG 4 (9 tokens, 4096 x 14336 Q8_0 87 us against 127
-// with KG 2), else KG 2 (101 tokens, 8192 x 4096 Q4_0 50 us against 73 with
-// KG 1).
+// fills the GPU, else TN 32.  bf16 x, 32 experts of 1536 x 2048, exactly 64 /
+// 96 / 128 / 192 / 256 tokens each: TN 128 45 / 46 / 48 / 83 / 85 us in Q4_0
+// and 53 / 56 / 58 / 91 / 94 in Q8_0, TN 32 34 / 52 / 61 / 110 / 116 and 53 /
+// 74 / 84 / 161 / 162.  A tile costs the same for 1 token as for 128: with
+// 128 tokens each on average half the experts take two, TN 128 89 (Q4_0) and
+// 93 (Q8_0) against 78 and 110; with 160 82 and 90 against 110 and 162.
+// Under that, 512 tokens through 6144 x 4096 (192 wide tiles): TN 128 68
+// (Q4_0) and 75 (Q8_0), TN 32 59 and 87.
+//
+// With TN 32, waves of a workgroup share rows (KG) where one per 32 rows and
+// tile would leave the SIMDs short of waves: as many as have all workgroups
+// on the GPU at once.  20 tokens, bf16, n x 4096, the number of waves on
+// either side of each border:
+//   KG 8 to 4 past 256   Q8_0 256: 17.2 / 18.4 us, 448: 31.8 / 24.2;  Q4_K 18.1 / 20.5, 32.9 / 26.0
+//   KG 4 to 2 past 512   Q8_0 512: 24.7 / 27.5, 576: 36.5 / 34.8;  Q4_0 20.1 / 22.5, 31.0 / 27.7;  Q6_K 28.7 / 32.3, 42.4 / 43.3
+//   KG 2 to 1 past 1024 in Q8_0 (two workgroups each, the others three)
+//                        1024: 36.4 / 41.1, 1152: 55.7 / 53.1
+//        past 1536       Q4_0 1536: 36.5 / 43.3, 1600: 50.3 / 43.3;  Q6_K 58.3 / 73.8, 78.2 / 73.9
+// 101 tokens with 40 adapters through 4096 x 14336 (512 waves): Q4_K KG 4 97,
+// KG 8 114, KG 2 115, Q8_0 82, 98, 102; through 14336 x 4096 (1792) KG 2 / 1
+// 90 / 78 and 87 / 73.  fp32 (a workgroup of KG 4 each):
+//   KG 4 to 2 past 256   Q8_0 256: 26.7 / 33.9, 448: 48.9 / 36.1
+//   KG 2 to 1 past 512 where LDS holds one workgroup (Q8_0, Q6_K)
+//                        Q8_0 512: 37.3 / 60.6, 576: 68.0 / 61.5
+//        from 2048       Q4_0 1536: 70.2 / 86.0, 2048 (n x 2048): 48.1 / 47.2;  Q4_K 2048: 55.5 / 49.2
 template <class F, class XT>
 int32_t launch_tile_n(const TileCall& c, hipStream_t st) {
     constexpr bool kWideX = std::is_same<XT, float>::value;
@@ -1268,13 +1283,15 @@ int32_t launch_tile_n(const TileCall& c, hipStream_t st) {
     // KG 4 and 8 have 16 gate rows and 16 up rows in a wave: their bytes have
     // to be within the 32-bit offsets from its first row
     const bool near = !c.swiglu || c.rows * (c.cols / 32) < (1ll << 25);
+    constexpr int kTwo = TileShape<F, XT, 32, 2>::kWgs;
     if constexpr (kWideX) {
         if (waves <= cus && near) return launch_tile_s<F, XT, 32, 4>(c, tile, st);
+        if (kTwo > 1 ? waves < 8 * cus : waves <= 2 * cus) return launch_tile_s<F, XT, 32, 2>(c, tile, st);
     } else {
         if (waves <= cus && near) return launch_tile_s<F, XT, 32, 8>(c, tile, st);
-        if (waves < 4 * cus && near) return launch_tile_s<F, XT, 32, 4>(c, tile, st);
+        if (waves <= 2 * cus && near) return launch_tile_s<F, XT, 32, 4>(c, tile, st);
+        if (waves <= 2 * kTwo * cus) return launch_tile_s<F, XT, 32, 2>(c, tile, st);
     }
-    if (waves < 8 * cus) return launch_tile_s<F, XT, 32, 2>(c, tile, st);
     return launch_tile_s<F, XT, 32, 1>(c, tile, st);
 }
 

@@ -18,7 +18,7 @@ def up(a, b):
     return -(-a // b)
 
 
-def tile_of(wide_x, items, E, matrix_rows):
+def tile_of(wide_x, fmt, items, E, matrix_rows):
     """(tokens of a tile, waves that share rows, parts of a plan's tile, whether its row tiles take more than one unit)."""
     tile = 128 if items >= 48 * E else 32
     groups, wide = min(E, items), 64 if wide_x else 128
@@ -26,26 +26,33 @@ def tile_of(wide_x, items, E, matrix_rows):
     if tile == 128 and groups * up(each, wide) * up(matrix_rows, 128) >= CUS:
         return wide, 1, tile // wide, up(matrix_rows, 128) > 32
     waves = groups * up(each, 32) * up(matrix_rows, 32)
+    # workgroups of two waves to a row that a compute unit holds
+    two = (1 if fmt in ("q8_0", "q6_k") else 2) if wide_x else 2 if fmt == "q8_0" else 3
     if wide_x:
-        kg = 4 if waves <= CUS else 2 if waves < 8 * CUS else 1
+        kg = 4 if waves <= CUS else 2 if (waves < 8 * CUS if two > 1 else waves <= 2 * CUS) else 1
     else:
-        kg = 8 if waves <= CUS else 4 if waves < 4 * CUS else 2 if waves < 8 * CUS else 1
+        kg = 8 if waves <= CUS else 4 if waves <= 2 * CUS else 2 if waves <= 2 * two * CUS else 1
     return 32, kg, tile // 32, up(matrix_rows, 128 // min(kg, 4)) > 32
 
 
 # items, experts, matrix rows
-CASES = [(120, 2, 1100), (240, 4, 1100), (480, 8, 2200), (600, 6, 4200), (520, 4, 8300), (30, 1, 1100), (90, 4, 2100), (90, 4, 8300),
+CASES = [(120, 2, 1100), (180, 3, 2100), (128, 2, 4200), (600, 6, 4200), (520, 4, 8300), (30, 1, 1100), (90, 4, 2700), (90, 4, 6300),
          (200, 8, 8300), (300, 1, 33100)]
 SHAPES = {False: {(128, 1, 1), (32, 1, 1), (32, 2, 1), (32, 4, 1), (32, 8, 1), (32, 1, 4), (32, 2, 4), (32, 4, 4), (32, 8, 4)},
-          # one wave to 32 rows of fp32 activations takes 2048 waves: split tiles have as many workgroups of 64 tokens then
+          # one wave to 32 rows takes 2048 waves where a compute unit holds two workgroups of two waves to a row: split tiles
+          # have as many workgroups of 64 tokens then
           True: {(64, 1, 2), (32, 1, 1), (32, 2, 1), (32, 4, 1), (32, 2, 4), (32, 4, 4)}}
 
 
+@pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("wide_x", [False, True])
-def test_the_cases_take_every_tile(wide_x):
-    got = {tile_of(wide_x, *c) for c in CASES}
-    assert {g[:3] for g in got} == SHAPES[wide_x]
-    assert {g[1] for g in got if g[2] > 1 and g[3]} == ({1, 2, 4} if wide_x else {1, 2, 4, 8})
+def test_the_cases_take_every_tile(wide_x, fmt):
+    got = {tile_of(wide_x, fmt, *c) for c in CASES}
+    want = SHAPES[wide_x]
+    if wide_x and fmt in ("q8_0", "q6_k"):
+        want = want | {(32, 1, 4)}
+    assert {g[:3] for g in got} == want
+    assert {g[1] for g in got if g[2] > 1 and g[3]} == {k for _, k, split in want if split > 1}
 
 
 def test_the_rule_is_the_sources():
@@ -54,9 +61,11 @@ def test_the_rule_is_the_sources():
     src = open(os.path.join(root, "qmv_tile.h")).read()
     body = re.sub(r"//[^\n]*", "", src[src.index("int32_t launch_tile_n("):src.index("int32_t launch_tile_x(")])
     said = [" ".join(m.split()) for m in re.findall(r"if \(((?:[^()]|\([^()]*\))*)\)\s*return launch_tile_s<F, XT, (?:\w+, \d+)>", body)]
-    assert said == ["tile == 128 && wide >= cus", "waves <= cus && near", "waves <= cus && near", "waves < 4 * cus && near",
-                    "waves < 8 * cus"], said
-    assert re.findall(r"return launch_tile_s<F, XT, (\w+, \d+)>", body) == ["kWide, 1", "32, 4", "32, 8", "32, 4", "32, 2", "32, 1"]
+    assert said == ["tile == 128 && wide >= cus", "waves <= cus && near", "kTwo > 1 ? waves < 8 * cus : waves <= 2 * cus",
+                    "waves <= cus && near", "waves <= 2 * cus && near", "waves <= 2 * kTwo * cus"], said
+    assert re.findall(r"return launch_tile_s<F, XT, (\w+, \d+)>", body) == ["kWide, 1", "32, 4", "32, 2", "32, 8", "32, 4", "32, 2", "32, 1"]
+    assert "kTwo = TileShape<F, XT, 32, 2>::kWgs;" in body
+    assert "kWgs = std::min(4 * kOcc / kWaves, kLdsMax / (kLds + 1024));" in src
     assert "kWideX ? 64 : 128" in body
     assert "constexpr int kRowGroup = 32;" in src
     group = open(os.path.join(root, "qmv_group.hip")).read()
@@ -90,7 +99,7 @@ def values(fmt, items, E, rows):
 @pytest.mark.parametrize("x_name", ["bf16", "f32"])
 def test_tiles(env, fmt, items, E, rows, x_name):  # noqa: F811
     torch, qmv = env
-    print("tiles", fmt, x_name, items, E, rows, tile_of(x_name == "f32", items, E, rows), flush=True)
+    print("tiles", fmt, x_name, items, E, rows, tile_of(x_name == "f32", fmt, items, E, rows), flush=True)
     (buf, stride, W), ids, xt, (y, e) = values(fmt, items, E, rows)
     K = xt.shape[1]
     x = (xt.float() if x_name == "f32" else xt).cuda()
