@@ -9,8 +9,8 @@
 //
 // 4096 x 4096 Q4_0, 1 token, rank 16: 4 + 5 + 4 us, all latency.  8 tokens of
 // 8 adapters, fp32, 6144 x 4096 Q8_0: 6 + 20 + 4, the FMA matvec's 8 columns.
-// 101 tokens of 40 requests, 4096 x 14336 Q4_K, rank 8: 14.5 for v (each
-// workgroup's adapters one after the other) and 93 for the tiles.
+// 101 tokens of 40 requests, 4096 x 14336 Q4_K, rank 8: 14 for v (each
+// workgroup's adapters one after the other) and 92 for the tiles.
 #include <algorithm>
 
 #include "qmv_tile.h"

@@ -20,13 +20,16 @@
 // columns (B), so that lane l holds results of one weight row, l % 32, for 16
 // tokens, and scales them all by one register.
 //
-// Many tokens (2048 through 14336 x 4096, bf16): Q4_0 392 us (613 TF/s), Q8_0
-// 420, Q4_K 499, Q6_K 584.  Of Q4_0's, MFMAs alone take 175; the scalings and
-// reads of x beside them make it 246, staging x adds 102, decoding 52,
-// staging weights 28: at two waves a SIMD these add up more than they
-// overlap.  Few tokens (single ones through experts of 8192 columns): weights
-// stream at 4.1 TB/s in Q8_0, 3.3 Q4_0, 3.1 Q6_K, 2.8 Q4_K, bound by decoding
-// and the LDS.
+// Many tokens (2048 through 14336 x 4096, bf16 in and out): Q4_0 336 us (716
+// TF/s), Q8_0 367, Q4_1 434, Q4_K 440, Q6_K 551.  Parts of Q4_0's left out in
+// turn (395 us with fp32 outputs): MFMAs alone 175, with the scalings and
+// reads of x beside them 246, staging x 102, decoding 52, staging weights 28:
+// at two waves a SIMD these add up more than they overlap (counters: vector
+// instructions 49% of the issue slots, the matrix pipe busy 25%).  Few tokens
+// (single ones through 128 experts of 2048 x 8192): weights stream at 5.0
+// TB/s in Q8_0, 4.0 Q4_0, 3.6 Q4_1 and Q6_K, 3.2 Q4_K; no pipe is full (with 9
+// tokens through 1536 x 2048 Q4_0 the vector pipe 47%, the matrix pipe 12%,
+// LDS bank conflicts 22% of the cycles).
 #pragma once
 #include <type_traits>
 

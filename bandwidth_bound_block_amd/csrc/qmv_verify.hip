@@ -14,10 +14,11 @@
 // request, and the chunk sums of the drawn row's weights; (3) the chunk and
 // the place in it.  (3) by the last workgroup of (2) took longer: the fences
 // it needs write the L2s back (139 us against 26 + 27 with the same bodies
-// for 64 requests of 151936 tokens).  There the three take 46, 22 and 11 us;
-// the first is bound by memory (fp32 logits of 64 x 1..8 rows at the copy
-// rate), the others by fp64 exponentials and by latency: 1 request of 4
-// drafts and 128256 tokens takes 4, 7 and 8 us.  Exponentials and sums are in
+// for 64 requests of 151936 tokens).  There the three take 47, 22 and 11 us;
+// the first reads 190 MB (fp32 logits of 64 x 1..8 rows) at 4.0 TB/s with 68%
+// of the vector issue slots taken by fp64 exponentials, the others are bound
+// by those and by latency: 1 request of 4 drafts and 128256 tokens takes 4, 6
+// and 8 us.  Exponentials and sums are in
 // fp64: the outputs are comparisons, and with fp32 sums (1e-7 off) over a
 // vocabulary of 1.5e5 about one draw in thirty could fall on the wrong side
 // of a border between two tokens of mean mass.
