@@ -33,6 +33,9 @@ Entry points (same names as the C ABI):
   qmv_moe_weighted_sum             router-weighted sum over a token's slots
   qmv_lora                         shared projection with a low-rank adapter per token
   qmv_spec_verify                  drafted tokens against the target's probabilities
+  qmv_cache_write / qmv_cache_read    keys and values into the pages of a quantized cache, and back (serving.py)
+  qmv_cache_attention              attention of new tokens over such a cache (serving.py)
+  qmv_logprobs                     log probabilities, entropy, most probable tokens (serving.py)
   qmv_dequant                      stored blocks -> fp32 (test/inspection aid)
   qmv_stream_read                  stream-read ceiling of the device (measurement aid)
   qmv_chain                        batch-1 matvec stages in one persistent launch
@@ -47,7 +50,8 @@ __all__ = ["QmvError", "qmv_q8_0", "qmv_q4_0", "qmv_q4_1", "qmv_q4_k", "qmv_q6_k
            "GroupPlan", "qmv_group_plan", "qmv_moe_grouped", "qmv_moe_grouped_swiglu", "qmv_moe_weighted_sum",
            "qmv_lora", "qmv_spec_verify",
            "qmv_dequant", "qmv_stream_read", "qmv_chain", "qmv_chain_noalloc", "ChainStage", "CHAIN_WORKSPACE_BYTES", "abi_version", "last_error",
-           "library_path", "lib", "Q8_0", "Q4_0", "Q4_1", "Q4_K", "Q6_K", "FORMATS", "BLOCK_BYTES", "row_bytes"]
+           "library_path", "lib", "Q8_0", "Q4_0", "Q4_1", "Q4_K", "Q6_K", "FORMATS", "BLOCK_BYTES", "row_bytes",
+           "KVCache", "Logprobs", "cache_page_bytes", "serving"]      # serving's own __all__ has its entry points
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "libqmv.so")
@@ -771,3 +775,10 @@ def qmv_chain_noalloc(fmt, stages, stream=None):
     argument, nothing allocated; see qmv.h).  stages as for qmv_chain."""
     arr = stages if isinstance(stages, ctypes.Array) else chain_stages(stages, fmt)
     _check(_lib.qmv_chain_noalloc(_fmt(fmt), ctypes.cast(arr, ctypes.c_void_p), len(arr), _stream(stream)))
+
+
+from . import serving  # noqa: E402
+from .serving import (KVCache, Logprobs, cache_page_bytes, qmv_cache_attention, qmv_cache_read, qmv_cache_write,  # noqa: E402
+                      qmv_logprobs)
+
+serving.bind(_lib)

@@ -1,0 +1,6 @@
+// The streaming attention kernel for Q4_0 keys and fp32 queries (two pieces).
+#include "qmv_attention.h"
+
+namespace qmv {
+int32_t attn_stream_q4_0_2(const AttnArgs& a, int D, hipStream_t st) { return launch_stream<QMV_Q4_0, 2>(a, D, st); }
+}  // namespace qmv

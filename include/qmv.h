@@ -598,6 +598,167 @@ int32_t qmv_spec_verify(const void* logits, int32_t logits_type, int64_t logits_
                         void* stream);
 
 /*
+ * A cache of keys and values in pages, block-quantized as the matrices are:
+ * blocks of 32 values of one token and key/value head, in QMV_Q8_0, QMV_Q4_0
+ * or QMV_Q4_1, keys and values each in their own format.  Token place s
+ * (a "slot") is place s % page_size of page s / page_size.  A page of
+ * format fmt holds, for each of its n_kv_heads heads behind each other, in
+ * page_size * (bytes of head_dim values) bytes:
+ *     codes     [page_size][head_dim * (8 or 4) / 8] bytes; in a row the
+ *               octet of values 32 b + 8 g .. + 7 lies at place
+ *               g * (head_dim / 32) + b: 8 signed bytes (Q8_0), or 4 bytes
+ *               with value 2 j in nibble j and value 2 j + 1 in nibble j + 4
+ *               (nibble 0 the low one of the first byte);
+ *     scales    fp16 [head_dim / 32][page_size];
+ *     minimums  fp16 [head_dim / 32][page_size] (Q4_1 only).
+ * The order gives each lane of a matrix-core step its values in one aligned
+ * load.  Values are those of the block formats: d*q, d*(c - 8), d*c + m.
+ *   k, v        device memory, n_pages pages each, 16-byte aligned; may be
+ *               one memory only where their pages do not overlap.
+ *   n_pages     >= 1, n_pages * page_size < 2^31;  n_kv_heads 1..1024;
+ *   head_dim    64, 128 or 256;  page_size a power of two, 16..4096.
+ *   reserved    0.
+ * The entry points that take a cache copy this host struct.
+ * qmv_cache_page_bytes: bytes of one page, a host function (0 for a format
+ * or size out of range).
+ */
+typedef struct {
+    void* k;
+    void* v;
+    int64_t n_pages;
+    int32_t k_fmt;
+    int32_t v_fmt;
+    int32_t n_kv_heads;
+    int32_t head_dim;
+    int32_t page_size;
+    int32_t reserved;
+} qmv_cache;
+
+size_t qmv_cache_page_bytes(qmv_fmt fmt, int32_t n_kv_heads, int32_t head_dim, int32_t page_size);
+
+/*
+ * Quantizes new keys and values into the cache: token t, head h into slot
+ * slots[t].  Per block of 32 values w, as the encoders of the matrices have
+ * it (round: to the nearest, halves away from zero):
+ *     Q8_0  d = fp16(max|w| / 127),      q = round(w / d) in -127..127
+ *     Q4_0  d = fp16(w_x / -8),          c = round(w / d) + 8 in 0..15, w_x
+ *           the value of largest magnitude (the first of them)
+ *     Q4_1  m = fp16(min), d = fp16((max - min) / 15),
+ *                                        c = round((w - m) / d) in 0..15
+ * with the quotient of d rounded to fp32 before it is rounded to fp16, and
+ * the codes those of the exact w / d.  d = 0 (never -0) gives codes that
+ * stand for 0 (m).  Values past +-65024 are stored as that (what DEQ gives then stays
+ * within fp16); a block with a NaN or an infinity reads back as NaN.
+ *   k, v      x_type (QMV_X_F32, QMV_X_F16, QMV_X_BF16) [n_tokens]
+ *             [n_kv_heads][head_dim], strides in elements: per token any,
+ *             per head >= head_dim where there is more than one.  16-byte
+ *             aligned with strides of whole 16 bytes they are read in
+ *             16-byte pieces.
+ *   slots     int32 [n_tokens], device memory.  A token whose slot is not in
+ *             [0, n_pages * page_size) is left out (padding); the others'
+ *             slots must differ.
+ *   n_tokens  1..2^24.
+ * Other slots' bytes are left as they were.
+ * Errors: QMV_EINVAL, QMV_EALIGN, QMV_EUNSUPPORTED (format), QMV_EHIP.
+ */
+int32_t qmv_cache_write(const qmv_cache* cache, const void* k, int64_t k_stride_token, int64_t k_stride_head,
+                        const void* v, int64_t v_stride_token, int64_t v_stride_head, int32_t x_type,
+                        const int32_t* slots, int64_t n_tokens, void* stream);
+
+/*
+ * The values of slots: k_out, v_out of out_type, contiguous [n_tokens]
+ * [n_kv_heads][head_dim], each rounded once from fp32; either may be null.
+ * A slot out of range gives quiet NaN.  A slot may occur more than once.
+ * Errors: as qmv_cache_write.
+ */
+int32_t qmv_cache_read(const qmv_cache* cache, const int32_t* slots, int64_t n_tokens, void* k_out, void* v_out,
+                       int32_t out_type, void* stream);
+
+/*
+ * Attention of new tokens over the cache, for many requests: single tokens
+ * (decode), drafted tokens under verification, pieces of prompts, mixed.
+ * Request r has the query tokens q_begin[r] .. q_begin[r + 1] - 1, n of them,
+ * and kv_lens[r] tokens in the cache, the query tokens' own keys and values
+ * among them as the last n (written before).  Query i stands at position
+ * p = kv_lens[r] - n + i and sees the positions j <= p, with a window > 0
+ * only j > p - window.  For query head h, with key/value head
+ * h / (n_heads / n_kv_heads):
+ *     s_j = scale * q . K_j,   o = sum_j e^(s_j) V_j / (sum_j e^(s_j) + e^(sinks[h])),
+ * the last term only where sinks is given.  A query that sees nothing gives 0.
+ *   q          x_type [n_tokens][n_heads][head_dim], strides in elements: per
+ *              token any, per head >= head_dim where there is more than one.
+ *   n_heads    a multiple of n_kv_heads, at most 1024 * n_kv_heads.
+ *   page_table int32 [n_requests][max_pages]: position j of request r is in
+ *              page page_table[r][j / page_size].  Entries of pages that no
+ *              query of the request sees are not read.
+ *   kv_lens    int32 [n_requests], 0 .. max_pages * page_size; a request
+ *              whose length is another gives quiet NaN.  An entry of the
+ *              table outside [0, n_pages) makes the queries that see such a
+ *              position quiet NaN.
+ *   q_begin    int32 [n_requests + 1], not decreasing, in 0..n_tokens; or
+ *              null: request r has tokens r * max_q .. (r + 1) * max_q - 1,
+ *              and n_tokens = n_requests * max_q.  All of these are device
+ *              memory.
+ *   max_q      the most query tokens of a request, 1..n_tokens; of a request
+ *              that has more, those past max_q are left out.
+ *   scale      finite, > 0;  window 0 (none) or > 0;  sinks fp32 [n_heads]
+ *              or null.
+ *   out        x_type [n_tokens][n_heads][head_dim], contiguous.  Rows of no
+ *              request are left as they were.
+ *   workspace  device memory of >= qmv_cache_attention_workspace_bytes(...)
+ *              bytes, 16-byte aligned; any contents; calls that share one must
+ *              not run concurrently (values pass between launches in it).
+ *   n_requests 1..65535;  n_tokens 1..2^24, times n_heads / n_kv_heads below
+ *              2^31;  max_pages >= 1, with max_pages * page_size <= 2^30.
+ * Nothing is read back to the host: a captured call may be replayed with
+ * other lengths, tables and q_begin (within max_q).
+ * Statistics and sums are fp32.  16-bit queries: codes are exact in the
+ * matrix cores' fp16, bf16 queries are scaled by a power of two per row to
+ * fp16 (exact for all elements within 2^-28 of the row's largest), weights
+ * and DEQ(V) are rounded to fp16, and so is DEQ(K) where a request has more
+ * than 32 rows of queries (query tokens times n_heads / n_kv_heads).  fp32
+ * queries: two fp16 pieces of each, 22 bits.  |DEQ(V)| must be within fp16's
+ * range, as qmv_cache_write has it.  A NaN in the cache reaches the queries
+ * that see it and no others.  The same call gives the same bits; the other
+ * requests' lengths can change the order of a query's sums, nothing else.
+ * Errors: QMV_EINVAL, QMV_EALIGN, QMV_EUNSUPPORTED (format), QMV_EHIP.
+ */
+size_t qmv_cache_attention_workspace_bytes(const qmv_cache* cache, int64_t n_requests, int64_t n_tokens,
+                                           int32_t n_heads, int64_t max_q);
+int32_t qmv_cache_attention(const qmv_cache* cache, const void* q, int32_t x_type, int64_t q_stride_token,
+                            int64_t q_stride_head, int64_t n_tokens, int32_t n_heads, const int32_t* page_table,
+                            int64_t max_pages, const int32_t* kv_lens, const int32_t* q_begin, int64_t n_requests,
+                            int64_t max_q, float scale, int32_t window, const float* sinks, void* out,
+                            void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Log probabilities under rows of logits: the step after the lm_head for a
+ * caller who asks what a token's probability was.  With p = softmax(row r):
+ *     logprobs[r][i] = log p(targets[r][i]),   entropy[r] = -sum p log p,
+ *     top_tokens[r], top_logprobs[r]: the top_k most probable tokens in
+ *     order, of equal ones the lowest first.
+ *   logits    logits_type [n_rows][vocab], rows ld elements apart, ld >= vocab.
+ *             -inf is a probability of 0 (log probability -inf).
+ *   targets   int32 [n_rows][n_targets], n_targets 0..1024 (0: targets and
+ *             logprobs may be null); one outside [0, vocab) gives quiet NaN.
+ *   entropy   fp32 [n_rows], or null.
+ *   top_k     0..32 (0: top_tokens and top_logprobs may be null).  Where fewer
+ *             tokens have a probability, the rest are token -1 at -inf.
+ *   n_rows 1..2^20, vocab 1..2^22, n_rows * vocab chunks of 4096 below 2^28.
+ *   workspace device memory of >= qmv_logprobs_workspace_bytes(...) bytes,
+ *             16-byte aligned; any contents; calls that share one must not
+ *             run concurrently (values pass between launches in it).
+ * A row of -inf throughout, or with NaN or +inf, gives NaN for all its values
+ * and tokens -1.  Sums are fp32 of terms relative to the row's largest, that
+ * one left out and log1p taken: no digits are lost where a row is certain.
+ * Errors: QMV_EINVAL, QMV_EALIGN, QMV_EHIP.
+ */
+size_t qmv_logprobs_workspace_bytes(int64_t n_rows, int64_t vocab, int32_t top_k);
+int32_t qmv_logprobs(const void* logits, int32_t logits_type, int64_t ld, int64_t n_rows, int64_t vocab,
+                     const int32_t* targets, int32_t n_targets, float* logprobs, float* entropy, int32_t top_k,
+                     int32_t* top_tokens, float* top_logprobs, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * Dequantize a whole matrix to fp32: out[i][j] = DEQ(W)[i][j], exactly (every
  * Q8_0/Q4_0 value and every Q4_1 value d*c + m whose bits span <= 24 is
  * representable in fp32; otherwise it is rounded to nearest even; a Q4_K
