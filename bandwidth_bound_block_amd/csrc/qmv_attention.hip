@@ -66,6 +66,8 @@ extern "C" int32_t qmv_cache_attention(const qmv_cache* cache, const void* q, in
     a.page_shift = log2_of(cache->page_size);
     a.H = cache->n_kv_heads;
     a.G = n_heads / cache->n_kv_heads;
+    a.g_shift = a.G > 1 ? 32 - __builtin_clz(a.G - 1) : 0;
+    a.g_mul = (uint32_t)(((uint64_t(1) << (31 + a.g_shift)) + a.G - 1) / a.G);
     a.R = (int32_t)n_requests;
     a.q = q;
     a.qst = q_stride_token;

@@ -163,7 +163,10 @@ __global__ __launch_bounds__(kCT) void cache_write_kernel(const CacheArgs a) {
                 bias = 0.f;
                 m = (_Float16)mn + (_Float16)0.f;
                 mf = (float)m;
-                d = (_Float16)(float)(((double)mx - (double)mn) / 15.0);
+                // two roundings, as for the other formats: the compiler makes one of the two casts
+                float q = (float)(((double)mx - (double)mn) / 15.0);
+                asm("" : "+v"(q));
+                d = (_Float16)q;
             }
             if ((float)d != 0.f) codes_of(w, (float)d, mf, -bias, 15.f - bias, c);
             else
