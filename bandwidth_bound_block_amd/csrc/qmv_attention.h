@@ -63,6 +63,8 @@ struct AttnArgs {
     int32_t x_type;
     // workspace of the streaming kernel
     int64_t* prefix;                // [R + 1]: blocks of all units before request r's; [R + 1]: a share's blocks
+    int32_t stream_to, tile_over;   // a request's rows up to which the streaming kernel takes it, over which the tile kernel
+    float* tile_part;               // split tiles: [splits][n_tokens][heads][D], then (maximum, sum) of each
     float* part;                    // [2 * shares][rows][D], then maxima and sums [2 * shares][rows] each
 };
 
@@ -77,6 +79,9 @@ int32_t attn_stream_q4_0_1(const AttnArgs& a, int D, hipStream_t st);
 int32_t attn_stream_q4_0_2(const AttnArgs& a, int D, hipStream_t st);
 int32_t attn_stream_q4_1_1(const AttnArgs& a, int D, hipStream_t st);
 int32_t attn_stream_q4_1_2(const AttnArgs& a, int D, hipStream_t st);
+// Per pieces: launch the kernel for many rows, its tiles split over the keys.
+int32_t attn_tile_1(const AttnArgs& a, int D, int splits, hipStream_t st);
+int32_t attn_tile_2(const AttnArgs& a, int D, int splits, hipStream_t st);
 
 namespace {
 
@@ -109,7 +114,8 @@ __device__ __forceinline__ Req request(const AttnArgs& a, int r) {
     o.lo = a.window > 0 ? (int)max((int64_t)0, (int64_t)o.len - o.n - a.window + 1) : 0;
     o.blk0 = o.lo / kABlock;
     o.nblk = max(1, (int)(((int64_t)o.len + kABlock - 1) / kABlock) - o.blk0);
-    o.tiles = (int)(((int64_t)o.n * a.G + 16 * NT - 1) / (16 * NT));     // n_tokens * G < 2^31
+    const int rows = o.n * a.G;                                          // n_tokens * G < 2^31
+    o.tiles = rows > a.stream_to ? 0 : (int)(((int64_t)rows + 16 * NT - 1) / (16 * NT));
     return o;
 }
 
@@ -1053,7 +1059,7 @@ int32_t launch_stream_n(const AttnArgs& a, hipStream_t st) {
     static_assert(shares <= kAShares);
     hipLaunchKernelGGL((attn_stream_kernel<KF, VF, P, NB, NT>), dim3(shares), dim3(kAT), 0, st, a);
     if (const int32_t e = check_launch(name)) return e;
-    const int64_t most = a.max_q * a.G;
+    const int64_t most = std::min<int64_t>(a.max_q * a.G, a.stream_to);
     const int rows = (int)std::min<int64_t>(16 * NT, most);
     const int64_t work = a.H * ((most + 16 * NT - 1) / (16 * NT)) * rows;
     const unsigned x = (unsigned)std::min<int64_t>(work, std::max<int64_t>(1, 65536 / a.R));

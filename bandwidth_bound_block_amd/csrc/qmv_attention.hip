@@ -17,6 +17,21 @@ size_t stream_bytes(const qmv_cache& c, int64_t R, int32_t heads, int64_t max_q)
     return round16((size_t)(R + 2) * 8) + (size_t)(2 * kAShares * rows * (c.head_dim + 2)) * 4;
 }
 
+// Rows of a request up to which the streaming kernel takes it.
+constexpr int kFewRows = 32;
+// Parts that the tile kernel's tiles are split into over the keys: where there
+// are fewer tiles than the GPU runs at once (two of a compute unit).
+int tile_splits(const qmv_cache& c, int64_t T, int32_t heads, int64_t max_q) {
+    const int64_t G = heads / c.n_kv_heads;
+    if (max_q * G <= kFewRows) return 0;
+    const int64_t tiles = c.n_kv_heads * ((T * G + 127) / 128);
+    return (int)std::min<int64_t>(std::max<int64_t>(1, 512 / tiles), 32);
+}
+size_t tile_bytes(const qmv_cache& c, int64_t T, int32_t heads, int64_t max_q) {
+    const int s = tile_splits(c, T, heads, max_q);
+    return s > 1 ? round16((size_t)s * T * heads * (c.head_dim + 2) * 4) : 0;
+}
+
 }  // namespace
 }  // namespace qmv
 
@@ -26,7 +41,7 @@ extern "C" size_t qmv_cache_attention_workspace_bytes(const qmv_cache* cache, in
     if (!cache || !qmv_cache_page_bytes(QMV_Q8_0, cache->n_kv_heads, cache->head_dim, cache->page_size) ||
         !sizes_ok(*cache, n_requests, n_tokens, n_heads, max_q))
         return 0;
-    return stream_bytes(*cache, n_requests, n_heads, max_q);
+    return stream_bytes(*cache, n_requests, n_heads, max_q) + tile_bytes(*cache, n_tokens, n_heads, max_q);
 }
 
 extern "C" int32_t qmv_cache_attention(const qmv_cache* cache, const void* q, int32_t x_type, int64_t q_stride_token,
@@ -87,7 +102,17 @@ extern "C" int32_t qmv_cache_attention(const qmv_cache* cache, const void* q, in
     a.prefix = static_cast<int64_t*>(workspace);
     a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + round16((size_t)(n_requests + 2) * 8));
     const hipStream_t st = as_stream(stream);
+    a.tile_part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + stream_bytes(*cache, n_requests, n_heads, max_q));
     const bool two = x_type == QMV_X_F32;
+    const int splits = tile_splits(*cache, n_tokens, n_heads, max_q);
+    // of many requests some may be short; one that may be long goes the one way
+    const bool both = splits > 0 && n_requests > 1;
+    a.stream_to = both ? kFewRows : INT32_MAX;
+    a.tile_over = both ? kFewRows : 0;
+    if (splits > 0) {
+        const int32_t e = two ? attn_tile_2(a, cache->head_dim, splits, st) : attn_tile_1(a, cache->head_dim, splits, st);
+        if (e != QMV_OK || !both || a.G > kFewRows) return e;
+    }
     switch (cache->k_fmt) {
     case QMV_Q8_0: return two ? attn_stream_q8_0_2(a, cache->head_dim, st) : attn_stream_q8_0_1(a, cache->head_dim, st);
     case QMV_Q4_0: return two ? attn_stream_q4_0_2(a, cache->head_dim, st) : attn_stream_q4_0_1(a, cache->head_dim, st);
