@@ -79,6 +79,8 @@ int32_t attn_stream_q4_0_1(const AttnArgs& a, int D, hipStream_t st);
 int32_t attn_stream_q4_0_2(const AttnArgs& a, int D, hipStream_t st);
 int32_t attn_stream_q4_1_1(const AttnArgs& a, int D, hipStream_t st);
 int32_t attn_stream_q4_1_2(const AttnArgs& a, int D, hipStream_t st);
+// Rows of a tile of the kernel for many rows.
+inline int tile_rows(int D, int32_t x_type) { return D * (x_type == QMV_X_F32 ? 2 : 1) <= 256 ? 256 : 128; }
 // Per pieces: launch the kernel for many rows, its tiles split over the keys.
 int32_t attn_tile_1(const AttnArgs& a, int D, int splits, hipStream_t st);
 int32_t attn_tile_2(const AttnArgs& a, int D, int splits, hipStream_t st);

@@ -19,16 +19,16 @@ size_t stream_bytes(const qmv_cache& c, int64_t R, int32_t heads, int64_t max_q)
 
 // Rows of a request up to which the streaming kernel takes it.
 constexpr int kFewRows = 32;
-// Parts that the tile kernel's tiles are split into over the keys: where there
-// are fewer tiles than the GPU runs at once (two of a compute unit).
-int tile_splits(const qmv_cache& c, int64_t T, int32_t heads, int64_t max_q) {
+// Parts that the tile kernel's tiles are split into over the keys, where there
+// are fewer tiles than the GPU runs at once.
+int tile_splits(const qmv_cache& c, int64_t T, int32_t heads, int64_t max_q, int32_t x_type) {
     const int64_t G = heads / c.n_kv_heads;
     if (max_q * G <= kFewRows) return 0;
-    const int64_t tiles = c.n_kv_heads * ((T * G + 127) / 128);
-    return (int)std::min<int64_t>(std::max<int64_t>(1, 512 / tiles), 32);
+    const int64_t rows = tile_rows(c.head_dim, x_type), tiles = c.n_kv_heads * ((T * G + rows - 1) / rows);
+    return (int)std::min<int64_t>(std::max<int64_t>(1, 256 / tiles), 32);
 }
 size_t tile_bytes(const qmv_cache& c, int64_t T, int32_t heads, int64_t max_q) {
-    const int s = tile_splits(c, T, heads, max_q);
+    const int s = std::max(tile_splits(c, T, heads, max_q, QMV_X_F32), tile_splits(c, T, heads, max_q, QMV_X_F16));
     return s > 1 ? round16((size_t)s * T * heads * (c.head_dim + 2) * 4) : 0;
 }
 
@@ -104,7 +104,7 @@ extern "C" int32_t qmv_cache_attention(const qmv_cache* cache, const void* q, in
     const hipStream_t st = as_stream(stream);
     a.tile_part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + stream_bytes(*cache, n_requests, n_heads, max_q));
     const bool two = x_type == QMV_X_F32;
-    const int splits = tile_splits(*cache, n_tokens, n_heads, max_q);
+    const int splits = tile_splits(*cache, n_tokens, n_heads, max_q, x_type);
     // of many requests some may be short; one that may be long goes the one way
     const bool both = splits > 0 && n_requests > 1;
     a.stream_to = both ? kFewRows : INT32_MAX;

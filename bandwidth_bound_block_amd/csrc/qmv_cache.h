@@ -45,9 +45,13 @@ __device__ __forceinline__ uint32_t as_u(f16x2 h) { return __builtin_bit_cast(ui
 __device__ __forceinline__ f16x2 h2(float v) { return f16x2{(_Float16)v, (_Float16)v}; }
 
 // Codes as exact fp16 integers.  1024 + c has c in its lowest mantissa bits.
-// The pair (values 2 j, 2 j + 1) of an octet of 4-bit codes, less `bias`.
+// The pair (values 2 j, 2 j + 1) of an octet of 4-bit codes, less `bias`.  Mask
+// and base from registers: one instruction takes both, which two constants do not.
 __device__ __forceinline__ f16x2 nibble_pair(uint32_t w, int j, float bias) {
-    return as_h2(((w >> (4 * j)) & 0x000f000fu) | 0x64006400u) - h2(1024.f + bias);
+    uint32_t mask = 0x000f000fu, base = 0x64006400u;
+    asm("" : "+s"(mask));
+    asm("" : "+v"(base));
+    return as_h2(((w >> (4 * j)) & mask) | base) - h2(1024.f + bias);
 }
 // Bytes lo and hi (0..3 of a, 4..7 of b) of signed codes, which the caller
 // has flipped to s + 128.
