@@ -27,9 +27,12 @@ int tile_splits(const qmv_cache& c, int64_t T, int32_t heads, int64_t max_q, int
     const int64_t rows = tile_rows(c.head_dim, x_type), tiles = c.n_kv_heads * ((T * G + rows - 1) / rows);
     return (int)std::min<int64_t>(std::max<int64_t>(1, 256 / tiles), 32);
 }
+// Room for the split tiles' rows.  The splits times the tiles are 256 at most, of
+// 256 rows at most, and a row is split 32 times at most: a bound that grows
+// with the sizes, as the splits themselves do not.
 size_t tile_bytes(const qmv_cache& c, int64_t T, int32_t heads, int64_t max_q) {
-    const int s = std::max(tile_splits(c, T, heads, max_q, QMV_X_F32), tile_splits(c, T, heads, max_q, QMV_X_F16));
-    return s > 1 ? round16((size_t)s * T * heads * (c.head_dim + 2) * 4) : 0;
+    if (max_q * (heads / c.n_kv_heads) <= kFewRows) return 0;
+    return round16((size_t)std::min<int64_t>(32 * T * heads, 256 * 256) * (c.head_dim + 2) * 4);
 }
 
 }  // namespace

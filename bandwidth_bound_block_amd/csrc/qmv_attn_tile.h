@@ -617,7 +617,7 @@ template <int D, int P, bool K8, bool V8>
 int32_t launch_tile_n(const AttnArgs& a, int splits, hipStream_t st) {
     const char* name = "qmv_cache_attention";
     const int64_t most = (a.max_q * a.G + Tile<D, P>::kRows - 1) / Tile<D, P>::kRows;
-    const int64_t x = std::min<int64_t>(most, std::max<int64_t>(1, (int64_t(1) << 23) / ((int64_t)a.H * a.R * splits)));
+    const int64_t x = std::min<int64_t>(most, std::max<int64_t>(1, (int64_t(1) << 22) / ((int64_t)a.H * a.R * splits)));
     hipLaunchKernelGGL((attn_tile_kernel<D, P, K8, V8>), dim3((unsigned)(x * a.H), a.R, splits), dim3(Tile<D, P>::kThreads), 0, st, a);
     if (const int32_t e = check_launch(name)) return e;
     if (splits == 1) return QMV_OK;

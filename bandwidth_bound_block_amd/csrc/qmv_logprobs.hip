@@ -6,13 +6,18 @@
 // A = sum e^z (-z): sums of terms of one sign, so fp32 keeps the digits of a
 // row that is nearly certain.
 //
-// Two launches: every chunk of 4096 logits gives its maximum, T and A relative
-// to it, and its top_k in order; then a workgroup per row joins the chunks.
-// Top tokens: each wave sorts its 64 lanes' maxima, the k-th of them is
-// reached by at least k logits, so only logits that reach the largest such
-// bound are candidates, a little more than k; their places are counted
-// against each other.
+// Two launches: every chunk of 4096 logits gives its maximum, T and A
+// relative to it, and the maxima of groups of 64 logits; then a workgroup per
+// row joins the chunks.  Top tokens: the top_k-th largest of those maxima is
+// reached by the top_k most probable tokens, so only the few groups whose
+// maximum reaches it have candidates, whose logits the second launch reads
+// again; places among the candidates are counted.  Candidates found in the
+// first launch (ballots and a sort of lanes' maxima in every chunk) took 299
+// us for 500 x 151936, where the two launches now take 35 us (the read of the
+// logits, 4.4 TB/s) and 13 us (reads that wait for one another); one row of
+// 128256 takes 4 and 7 us.
 #include <algorithm>
+#include <type_traits>
 
 #include "qmv_block_decode.h"
 #include "qmv_host.h"
@@ -20,12 +25,18 @@
 namespace qmv {
 namespace {
 
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
 constexpr int kLT = 256;
 constexpr int kLWaves = kLT / 64;
+// Logits of a thread: with 64 the first launch took 5.9 us for one row of
+// 128256, with 16 it takes 4.0; 500 rows of 151936 take 50.4 us with 64 and
+// 48.8 with 16, both launches.
 constexpr int kLPer = 16;
-constexpr int kLChunk = kLT * kLPer;
+constexpr int kLGroup = 64;                   // logits of a group: those of kLGroup / kLPer threads
 constexpr int kLTop = 32;
-constexpr int kLCands = 2048;            // candidates of a row that are counted in LDS
+constexpr int kLCands = 1024;                 // groups that reach the bound, and candidates, of a row that LDS holds
+constexpr int kLKeep = 16;                    // maxima of groups that a thread keeps in registers
 
 struct ChunkStat {
     float m, t, a;       // maximum; sum of e^(l - m) without one largest term; sum of e^(l - m) (m - l).  NaN in t: no distribution
@@ -34,7 +45,7 @@ struct ChunkStat {
 struct LogprobArgs {
     const void* logits;
     int64_t ld, rows;
-    int V, chunks, top, vec;
+    int V, chunks, top;
     const int32_t* targets;
     int n_targets;
     float* logprobs;
@@ -42,18 +53,28 @@ struct LogprobArgs {
     int32_t* top_tokens;
     float* top_logprobs;
     ChunkStat* stat;     // [rows][chunks]
-    float* best;         // [rows][chunks][top]: largest logits in order, then -inf
-    int32_t* best_id;
+    float* most;         // [rows][chunks][groups]: largest logit of each group
 };
 
-// e^x for x <= 0, relative error about 2^-22: x log2(e) in two parts, since an
-// error of the exponent is one of the result.
-__device__ __forceinline__ float exp_neg32(float x) {
-    const float hi = x * 1.44269504088896341f;
-    const float lo = __builtin_fmaf(x, 1.44269504088896341f, -hi) + x * 1.92596299e-8f;
-    // x = -inf: lo is NaN, and the result 0
-    return hi < -160.f ? 0.f : __builtin_amdgcn_exp2f(hi) * __builtin_fmaf(lo, 0.69314718f, 1.f);
+// Pieces of 16 bytes of a row: thread t of a chunk has pieces t, t + 256, ..  A
+// row may begin at any element; the hardware takes such addresses.
+template <class LT> constexpr int kVecOf = 16 / sizeof(LT);
+typedef uint32_t piece_a4 __attribute__((ext_vector_type(4), aligned(4)));
+typedef uint32_t piece_a2 __attribute__((ext_vector_type(4), aligned(2)));
+template <class LT>
+__device__ __forceinline__ u32x4 load_piece(const LT* p) {
+    if constexpr (sizeof(LT) == 4) return *reinterpret_cast<const piece_a4*>(p);
+    else return *reinterpret_cast<const piece_a2*>(p);
 }
+
+// e^z for z <= 0, and 0 for what is below -1000: the rounding of z log2(e) is a
+// relative error of |z| 2^-24.
+__device__ __forceinline__ float exp_neg32(float z) {
+    return __builtin_amdgcn_exp2f(fmaxf(z, -1000.f) * 1.44269504088896341f);
+}
+
+// The larger one, NaN if either is.
+__device__ __forceinline__ float max_or_nan(float a, float b) { return __builtin_elementwise_maximum(a, b); }
 
 __device__ __forceinline__ float wave_sum(float s) {
 #pragma unroll
@@ -64,6 +85,15 @@ __device__ __forceinline__ float wave_max(float m) {
 #pragma unroll
     for (int o = 32; o; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
     return m;
+}
+// A number that grows with x, and for equal x with a smaller id; +0 and -0 are equal.
+__device__ __forceinline__ uint64_t order_key(float x, int id) {
+    const uint32_t u = __builtin_bit_cast(uint32_t, x + 0.f);
+    return (uint64_t)(u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u)) << 32 | ~(uint32_t)id;
+}
+__device__ __forceinline__ float key_value(uint64_t key) {
+    const uint32_t u = (uint32_t)(key >> 32);
+    return __builtin_bit_cast(float, u & 0x80000000u ? u ^ 0x80000000u : ~u);
 }
 // Every lane gets a wave's values in descending order.
 __device__ __forceinline__ float wave_sort(float v) {
@@ -81,59 +111,88 @@ __device__ __forceinline__ float wave_sort(float v) {
 
 template <class LT>
 __global__ __launch_bounds__(kLT) void logprobs_chunk_kernel(const LogprobArgs a) {
-    const int c = blockIdx.x;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    constexpr int kVec = kVecOf<LT>, kN = kLPer / kVec;
+    const int c = blockIdx.x, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const float inf = __builtin_inff();
-    __shared__ float wm[kLWaves], wt[kLWaves], wa[kLWaves], wb[kLWaves], wc[kLWaves];
-    __shared__ int wbad[kLWaves], s_n;
-    __shared__ float s_v[kLChunk];
-    __shared__ int s_id[kLChunk];
+    __shared__ float wm[kLWaves], wt[kLWaves], wa[kLWaves], wc[kLWaves];
     for (int64_t row = blockIdx.y; row < a.rows; row += gridDim.y) {
         const LT* l = static_cast<const LT*>(a.logits) + row * a.ld;
-        const int v0 = c * kLChunk;
+        const int u0 = c * (kLT * kLPer) + kVec * (int)threadIdx.x;
         float f[kLPer];
+        u32x4 w[kN];
+        const bool whole = (c + 1) * (kLT * kLPer) <= a.V;
 #pragma unroll
-        for (int k = 0; k < kLPer / 4; ++k) {
-            const int v = v0 + 4 * ((int)threadIdx.x + kLT * k);
-            if (a.vec && v + 3 < a.V) {
-                const float4 w = XIn<LT>::load4(l + v);
-                f[4 * k] = w.x; f[4 * k + 1] = w.y; f[4 * k + 2] = w.z; f[4 * k + 3] = w.w;
-            } else {
+        for (int k = 0; k < kN; ++k) {
+            const int u = u0 + kVec * kLT * k;
+            if (whole || u + kVec <= a.V) {
+                w[k] = load_piece(l + u);
+            } else {                       // the row's last piece, or one behind it
+                constexpr uint32_t none = sizeof(LT) == 4 || std::is_same_v<LT, __bf16> ? 0xff80u : 0xfc00u;      // -inf's high half
 #pragma unroll
-                for (int j = 0; j < 4; ++j) f[4 * k + j] = v + j < a.V ? XIn<LT>::load1(l + v + j) : -inf;
+                for (int j = 0; j < 4; ++j) {
+                    if constexpr (sizeof(LT) == 4) {
+                        w[k][j] = u + j < a.V ? reinterpret_cast<const uint32_t*>(l)[u + j] : none << 16;
+                    } else {
+                        const uint16_t* b = reinterpret_cast<const uint16_t*>(l) + u + 2 * j;
+                        w[k][j] = (u + 2 * j < a.V ? b[0] : none) | (u + 2 * j + 1 < a.V ? b[1] : none) << 16;
+                    }
+                }
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < kN; ++k) {
+            const u32x4 x = w[k];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t y = x[j];
+                if constexpr (sizeof(LT) == 4) {
+                    f[4 * k + j] = __builtin_bit_cast(float, y);
+                } else if constexpr (std::is_same_v<LT, _Float16>) {
+                    f[8 * k + 2 * j] = half_bits_to_float(y);
+                    f[8 * k + 2 * j + 1] = half_bits_to_float(y >> 16);
+                } else {
+                    f[8 * k + 2 * j] = __builtin_bit_cast(float, y << 16);
+                    f[8 * k + 2 * j + 1] = __builtin_bit_cast(float, y & 0xffff0000u);
+                }
             }
         }
         float mine = -inf;
-        bool bad = false;
 #pragma unroll
-        for (int i = 0; i < kLPer; ++i) {
-            mine = fmaxf(mine, f[i]);
-            bad |= !(f[i] < inf);
+        for (int i = 0; i < kLPer; ++i) mine = max_or_nan(mine, f[i]);
+        const int64_t at = row * a.chunks + c;
+        if (a.top) {
+            constexpr int kThreads = kLGroup / kLPer;
+            float g = mine;
+#pragma unroll
+            for (int o = 1; o < kThreads; o <<= 1) g = fmaxf(g, __shfl_xor(g, o));
+            if (threadIdx.x % kThreads == 0) a.most[at * (kLT / kThreads) + threadIdx.x / kThreads] = g;
         }
-        float m = wave_max(mine);
-        float bound = -inf;
-        if (a.top) bound = __shfl(wave_sort(mine), a.top - 1);
+        float m = mine;
+#pragma unroll
+        for (int o = 32; o; o >>= 1) m = max_or_nan(m, __shfl_xor(m, o));
         __syncthreads();          // the last row's reads
-        if (lane == 0) {
-            wm[wave] = m;
-            wb[wave] = bound;
-        }
-        bad = __any(bad);
-        if (lane == 0) wbad[wave] = bad;
-        if (threadIdx.x == 0) s_n = 0;
+        if (lane == 0) wm[wave] = m;
         __syncthreads();
-        m = fmaxf(fmaxf(wm[0], wm[1]), fmaxf(wm[2], wm[3]));
-        bound = fmaxf(fmaxf(wb[0], wb[1]), fmaxf(wb[2], wb[3]));
-        bad = wbad[0] | wbad[1] | wbad[2] | wbad[3];
+        m = max_or_nan(max_or_nan(wm[0], wm[1]), max_or_nan(wm[2], wm[3]));
+        // largest terms are 1 each and are counted: beside them the small ones would lose their digits
         float t = 0.f, e_a = 0.f;
         int tops = 0;
-        if (m > -inf) {
+        const bool good = m > -inf && m < inf;
+        if (good && __any(mine == m)) {
 #pragma unroll
             for (int i = 0; i < kLPer; ++i) {
-                const float z = f[i] - m, e = exp_neg32(z);
-                tops += f[i] == m;
-                t += f[i] == m ? 0.f : e;
-                e_a += e > 0.f ? e * -z : 0.f;
+                const float z = fmaxf(f[i] - m, -1000.f), e = __builtin_amdgcn_exp2f(z * 1.44269504088896341f);
+                const bool top = z == 0.f;
+                tops += top;
+                t += top ? 0.f : e;
+                e_a = __builtin_fmaf(e, -z, e_a);
+            }
+        } else if (good) {        // most waves: what is left out here was a third of the launch's instructions
+#pragma unroll
+            for (int i = 0; i < kLPer; ++i) {
+                const float z = fmaxf(f[i] - m, -1000.f), e = __builtin_amdgcn_exp2f(z * 1.44269504088896341f);
+                t += e;
+                e_a = __builtin_fmaf(e, -z, e_a);
             }
         }
         t = wave_sum(t);
@@ -144,81 +203,61 @@ __global__ __launch_bounds__(kLT) void logprobs_chunk_kernel(const LogprobArgs a
             wa[wave] = e_a;
             wc[wave] = count;
         }
-        if (a.top) {
-            // candidates, those equal to the bound among them
-#pragma unroll
-            for (int i = 0; i < kLPer; ++i) {
-                const bool in = f[i] >= bound && f[i] > -inf;
-                const uint64_t who = __ballot(in);
-                if (!who) continue;
-                int at = 0;
-                if (lane == __builtin_ctzll(who)) at = atomicAdd(&s_n, __popcll(who));
-                at = __builtin_amdgcn_readlane(at, __builtin_ctzll(who)) + __builtin_popcountll(who & ((uint64_t(1) << lane) - 1));
-                if (in) {
-                    s_v[at] = f[i];
-                    s_id[at] = v0 + 4 * ((int)threadIdx.x + kLT * (i >> 2)) + (i & 3);
-                }
-            }
-        }
         __syncthreads();
-        const int64_t at = row * a.chunks + c;
         if (threadIdx.x == 0) {
             ChunkStat s;
             s.m = m;
-            // the other largest terms, each 1, come last: beside 1 the small ones would lose their digits
-            s.t = bad ? __builtin_nanf("")
-                  : m > -inf ? (wt[0] + wt[1]) + (wt[2] + wt[3]) + (wc[0] + wc[1] + wc[2] + wc[3] - 1.f) : 0.f;
+            s.t = good ? (wt[0] + wt[1]) + (wt[2] + wt[3]) + (wc[0] + wc[1] + wc[2] + wc[3] - 1.f)
+                  : m == -inf ? 0.f : __builtin_nanf("");
             s.a = (wa[0] + wa[1]) + (wa[2] + wa[3]);
             s.pad = 0.f;
             a.stat[at] = s;
-        }
-        if (a.top) {
-            const int n = s_n;
-            for (int i = threadIdx.x; i < n; i += kLT) {
-                const float v = s_v[i];
-                const int id = s_id[i];
-                int place = 0;
-                for (int j = 0; j < n; ++j) place += s_v[j] > v || (s_v[j] == v && s_id[j] < id);
-                if (place < a.top) {
-                    a.best[at * a.top + place] = v;
-                    a.best_id[at * a.top + place] = id;
-                }
-            }
-            for (int i = n + threadIdx.x; i < a.top; i += kLT) {
-                a.best[at * a.top + i] = -inf;
-                a.best_id[at * a.top + i] = -1;
-            }
         }
     }
 }
 
 template <class LT>
 __global__ __launch_bounds__(kLT) void logprobs_row_kernel(const LogprobArgs a) {
+    constexpr int kVec = kVecOf<LT>, kThreads = kLGroup / kLPer, kGroups = kLT / kThreads, kPieces = kLGroup / kVec;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const float inf = __builtin_inff();
-    __shared__ float s_m, s_log, s_bad, s_b[kLWaves], s_v[kLCands];
-    __shared__ int s_n, s_id[kLCands];
+    __shared__ float s_m, s_log, s_bad, s_bound;
+    __shared__ __align__(16) float s_b[kLWaves * kLTop];
+    __shared__ __align__(16) uint64_t s_key[kLCands];
+    __shared__ int s_n, s_c, s_id[kLCands];
     for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
         const ChunkStat* st = a.stat + row * a.chunks;
+        const float* most = a.most + row * a.chunks * kGroups;
+        const int groups = a.top ? a.chunks * kGroups : 0;
+        float g[kLKeep];      // on their way while the chunks are joined
+#pragma unroll
+        for (int k = 0; k < kLKeep; ++k) {
+            const int i = threadIdx.x + k * kLT;
+            g[k] = i < groups ? most[i] : -inf;
+        }
+        const LT* l = static_cast<const LT*>(a.logits) + row * a.ld;
+        int target = -1;
+        if ((int)threadIdx.x < a.n_targets) target = a.targets[row * a.n_targets + threadIdx.x];
+        const float l_target = (unsigned)target < (unsigned)a.V ? XIn<LT>::load1(l + target) : __builtin_nanf("");
         __syncthreads();
         if (wave == 0) {
-            float m = -inf, bad = 0.f;
-            for (int c = lane; c < a.chunks; c += 64) {
+            const ChunkStat none = {-inf, 0.f, 0.f, 0.f}, first = lane < a.chunks ? st[lane] : none;
+            float m = first.m, bad = first.t >= 0.f ? 0.f : 1.f;
+            int lead = lane;      // the first chunk with the largest gives the term left out
+            for (int c = lane + 64; c < a.chunks; c += 64) {
+                if (st[c].m > m) lead = c;
                 m = fmaxf(m, st[c].m);
                 if (!(st[c].t >= 0.f)) bad = 1.f;
             }
+            const float own = m;
             m = wave_max(m);
-            bad = wave_max(bad);
-            if (!(m > -inf)) bad = 1.f;
-            // the first chunk with the largest gives the term left out
-            int lead = 0x7fffffff;
-            for (int c = lane; c < a.chunks; c += 64)
-                if (st[c].m == m && c < lead) lead = c;
+            bad = __any(bad != 0.f) || !(m > -inf) ? 1.f : 0.f;
+            if (own != m) lead = 0x7fffffff;
 #pragma unroll
             for (int o = 32; o; o >>= 1) lead = min(lead, __shfl_xor(lead, o));
             float t = 0.f, e_a = 0.f;
             for (int c = lane; c < a.chunks; c += 64) {
-                const ChunkStat s = st[c];
+                const ChunkStat s = c < 64 ? first : st[c];
                 if (!(s.m > -inf)) continue;
                 const float z = s.m - m, e = exp_neg32(z), all = 1.f + s.t;
                 t += c == lead ? s.t : e * all;
@@ -231,69 +270,96 @@ __global__ __launch_bounds__(kLT) void logprobs_row_kernel(const LogprobArgs a) 
                 s_m = m;
                 s_log = log_t;
                 s_bad = bad;
+                s_n = s_c = 0;
                 if (a.entropy) a.entropy[row] = bad != 0.f ? __builtin_nanf("") : log_t + e_a / (1.f + t);
             }
         }
+        // the top-th largest of the threads' maxima, each of a group of its own, bounds the row's from below
+        if (a.top) {
+            float mine = g[0];
+#pragma unroll
+            for (int k = 1; k < kLKeep; ++k) mine = fmaxf(mine, g[k]);
+            for (int i = threadIdx.x + kLKeep * kLT; i < groups; i += kLT) mine = fmaxf(mine, most[i]);
+            mine = wave_sort(mine);
+            if (lane < a.top) s_b[wave * a.top + lane] = mine;
+        }
         __syncthreads();
+        if ((int)threadIdx.x < kLWaves * a.top) {
+            const float v = s_b[threadIdx.x];
+            int place = 0;
+#pragma unroll 4
+            for (int j = 0; j < a.top; ++j) {
+                const f32x4 o = reinterpret_cast<const f32x4*>(s_b)[j];
+#pragma unroll
+                for (int k = 0; k < kLWaves; ++k) place += o[k] > v || (o[k] == v && kLWaves * j + k < (int)threadIdx.x);
+            }
+            if (place == a.top - 1) s_bound = v;
+        }
         const float m = s_m, log_t = s_log;
         const bool bad = s_bad != 0.f;
         for (int i = threadIdx.x; i < a.n_targets; i += kLT) {
             const int64_t at = row * a.n_targets + i;
-            const int x = a.targets[at];
-            float v = __builtin_nanf("");
-            if (!bad && (unsigned)x < (unsigned)a.V)
-                v = (XIn<LT>::load1(static_cast<const LT*>(a.logits) + row * a.ld + x) - m) - log_t;
-            a.logprobs[at] = v;
+            float v = l_target;
+            if (i >= kLT) {
+                const int x = a.targets[at];
+                v = (unsigned)x < (unsigned)a.V ? XIn<LT>::load1(l + x) : __builtin_nanf("");
+            }
+            a.logprobs[at] = bad ? __builtin_nanf("") : (v - m) - log_t;
         }
         if (!a.top) continue;
         const int64_t out = row * a.top;
-        const float* best = a.best + row * a.chunks * a.top;
-        const int* best_id = a.best_id + row * a.chunks * a.top;
-        // entries of the chunks' lists that reach the top-th of a wave's chunk maxima
-        if (threadIdx.x == 0) s_n = 0;
-        float mine = -inf;
-        for (int c = threadIdx.x; c < a.chunks; c += kLT) mine = fmaxf(mine, st[c].m);
-        const float bound = __shfl(wave_sort(mine), a.top - 1);
-        if (lane == 0) s_b[wave] = bound;
         __syncthreads();
-        const float reach = fmaxf(fmaxf(s_b[0], s_b[1]), fmaxf(s_b[2], s_b[3]));
-        const int entries = bad ? 0 : a.chunks * a.top;
-        for (int i = threadIdx.x; i < entries; i += kLT) {
-            const float v = best[i];
-            if (v >= reach && v > -inf) {
-                const int at = atomicAdd(&s_n, 1);
-                if (at < kLCands) {
-                    s_v[at] = v;
-                    s_id[at] = best_id[i];
+        const float bound = s_bound;
+        auto reached = [&](float v, int i) {
+            if (bad || !(v >= bound && v > -inf)) return;
+            const int at = atomicAdd(&s_n, 1);
+            if (at < kLCands) s_id[at] = i;
+        };
+#pragma unroll
+        for (int k = 0; k < kLKeep; ++k) reached(g[k], threadIdx.x + k * kLT);
+        for (int i = threadIdx.x + kLKeep * kLT; i < groups; i += kLT) reached(most[i], i);
+        __syncthreads();
+        int n = s_n;
+        // the groups' logits that reach it, piece by piece
+        for (int w = threadIdx.x; w < (n <= kLCands ? n * kPieces : 0); w += kLT) {
+            const int i = s_id[w / kPieces], k = w % kPieces;
+            const int id = i / kGroups * (kLT * kLPer) + kVec * (i % kGroups * kThreads + k % kThreads + kLT * (k / kThreads));
+            float x[kVec];
+#pragma unroll
+            for (int j = 0; j < kVec; ++j) x[j] = id + j < a.V ? XIn<LT>::load1(l + id + j) : -inf;
+#pragma unroll
+            for (int j = 0; j < kVec; ++j)
+                if (x[j] >= bound && x[j] > -inf) {
+                    const int at = atomicAdd(&s_c, 1);
+                    if (at < kLCands) s_key[at] = order_key(x[j], id + j);
                 }
-            }
         }
         __syncthreads();
-        const int n = s_n;
-        if (n <= kLCands) {      // the order they came in does not matter: a place is a count
+        const int found = s_c;
+        if (n <= kLCands && found <= kLCands) {      // the order they came in does not matter: a place is a count
+            n = found;
             for (int i = threadIdx.x; i < n; i += kLT) {
-                const float v = s_v[i];
-                const int id = s_id[i];
+                const uint64_t key = s_key[i];
                 int place = 0;
-                for (int j = 0; j < n; ++j) place += s_v[j] > v || (s_v[j] == v && s_id[j] < id);
+#pragma unroll 4
+                for (int j = 0; j < n; ++j) place += s_key[j] > key;
                 if (place < a.top) {
-                    a.top_tokens[out + place] = id;
-                    a.top_logprobs[out + place] = (v - m) - log_t;
+                    a.top_tokens[out + place] = (int)~(uint32_t)key;
+                    a.top_logprobs[out + place] = (key_value(key) - m) - log_t;
                 }
             }
-        } else if (wave == 0) {
-            // many equal ones: the largest behind the last one taken, top times
+        } else {
+            // many equal ones: the largest of the row behind the last one taken, top times
             float last_v = inf;
             int last_id = -1;
-            for (int k = 0; k < a.top; ++k) {
+            for (n = 0; n < a.top; ++n) {
                 float v = -inf;
                 int id = 0x7fffffff;
-                for (int i = lane; i < entries; i += 64) {
-                    const float x = best[i];
-                    const int y = best_id[i];
-                    if ((x < last_v || (x == last_v && y > last_id)) && (x > v || (x == v && y < id))) {
+                for (int i = threadIdx.x; i < a.V; i += kLT) {
+                    const float x = XIn<LT>::load1(l + i);
+                    if ((x < last_v || (x == last_v && i > last_id)) && x > v) {       // the first of equal ones: i goes up
                         v = x;
-                        id = y;
+                        id = i;
                     }
                 }
 #pragma unroll
@@ -305,9 +371,21 @@ __global__ __launch_bounds__(kLT) void logprobs_row_kernel(const LogprobArgs a) 
                         id = oi;
                     }
                 }
+                __syncthreads();
                 if (lane == 0) {
-                    a.top_tokens[out + k] = id;
-                    a.top_logprobs[out + k] = (v - m) - log_t;
+                    s_b[wave] = v;
+                    s_id[wave] = id;
+                }
+                __syncthreads();
+                for (int w = 0; w < kLWaves; ++w)
+                    if (s_b[w] > v || (s_b[w] == v && s_id[w] < id)) {
+                        v = s_b[w];
+                        id = s_id[w];
+                    }
+                if (!(v > -inf)) break;
+                if (threadIdx.x == 0) {
+                    a.top_tokens[out + n] = id;
+                    a.top_logprobs[out + n] = (v - m) - log_t;
                 }
                 last_v = v;
                 last_id = id;
@@ -321,7 +399,9 @@ __global__ __launch_bounds__(kLT) void logprobs_row_kernel(const LogprobArgs a) 
 }
 
 constexpr int64_t kLRows = 1 << 20, kLVocab = 1 << 22;
-int64_t chunks_of(int64_t vocab) { return (vocab + kLChunk - 1) / kLChunk; }
+int64_t chunks_of(int64_t vocab) {
+    return (vocab + kLT * kLPer - 1) / (kLT * kLPer);
+}
 bool sizes_ok(int64_t rows, int64_t vocab, int32_t top) {
     return rows >= 1 && rows <= kLRows && vocab >= 1 && vocab <= kLVocab && rows * chunks_of(vocab) < (1 << 28) && top >= 0 &&
            top <= kLTop;
@@ -342,7 +422,7 @@ int32_t launch_logprobs(const LogprobArgs& a, hipStream_t st) {
 extern "C" size_t qmv_logprobs_workspace_bytes(int64_t n_rows, int64_t vocab, int32_t top_k) {
     using namespace qmv;
     if (!sizes_ok(n_rows, vocab, top_k)) return 0;
-    return (size_t)(n_rows * chunks_of(vocab)) * (sizeof(ChunkStat) + 8 * (size_t)top_k);
+    return (size_t)(n_rows * chunks_of(vocab)) * (sizeof(ChunkStat) + (top_k ? 4 * (size_t)(kLT * kLPer / kLGroup) : 0));
 }
 
 extern "C" int32_t qmv_logprobs(const void* logits, int32_t logits_type, int64_t ld, int64_t n_rows, int64_t vocab,
@@ -373,7 +453,6 @@ extern "C" int32_t qmv_logprobs(const void* logits, int32_t logits_type, int64_t
     a.V = (int)vocab;
     a.chunks = (int)chunks_of(vocab);
     a.top = top_k;
-    a.vec = aligned(logits, 4 * le) && (n_rows == 1 || ld % 4 == 0);
     a.targets = targets;
     a.n_targets = n_targets;
     a.logprobs = logprobs;
@@ -381,8 +460,7 @@ extern "C" int32_t qmv_logprobs(const void* logits, int32_t logits_type, int64_t
     a.top_tokens = top_tokens;
     a.top_logprobs = top_logprobs;
     a.stat = static_cast<ChunkStat*>(workspace);
-    a.best = reinterpret_cast<float*>(a.stat + n_rows * a.chunks);
-    a.best_id = reinterpret_cast<int32_t*>(a.best + n_rows * a.chunks * top_k);
+    a.most = reinterpret_cast<float*>(a.stat + n_rows * a.chunks);
     const hipStream_t st = as_stream(stream);
     switch (logits_type) {
     case QMV_X_F32: return launch_logprobs<float>(a, st);
