@@ -11,8 +11,11 @@
 // into the operand of the second: with two tiles t of 16 keys, a lane has
 // after the first product the keys 16 t + 4 g + r (g = lane / 16, r < 4) of
 // query lane % 16, and the second takes in lane group g eight keys in any
-// order as long as both operands have the same.  fp32 queries, weights and
-// values are pairs of fp16 pieces.
+// order as long as both operands have the same.  With bf16 queries the weights
+// and values are rounded to fp16 (2^-11; the outputs to 2^-8).  With fp16 or
+// fp32 queries they are pairs of fp16 pieces, fp32 queries too: fp16 outputs
+// had twice the error of their own rounding without.  That costs little here
+// (131000 tokens: 44 us) and twice the time where arithmetic is the bound.
 //
 // The transposition that V needs (a lane multiplies eight keys of one place of
 // the head) happens inside the lane: it loads the same few values of its eight
@@ -80,7 +83,7 @@ int32_t attn_stream_q4_0_2(const AttnArgs& a, int D, hipStream_t st);
 int32_t attn_stream_q4_1_1(const AttnArgs& a, int D, hipStream_t st);
 int32_t attn_stream_q4_1_2(const AttnArgs& a, int D, hipStream_t st);
 // Rows of a tile of the kernel for many rows.
-inline int tile_rows(int D, int32_t x_type) { return D * (x_type == QMV_X_F32 ? 2 : 1) <= 256 ? 256 : 128; }
+inline int tile_rows(int D, int32_t x_type) { return D * (x_type == QMV_X_BF16 ? 1 : 2) <= 256 ? 256 : 128; }
 // Per pieces: launch the kernel for many rows, its tiles split over the keys.
 int32_t attn_tile_1(const AttnArgs& a, int D, int splits, hipStream_t st);
 int32_t attn_tile_2(const AttnArgs& a, int D, int splits, hipStream_t st);
@@ -204,40 +207,44 @@ __device__ __forceinline__ Share find_share(const AttnArgs& a, int wg, int wgs) 
     return s;
 }
 
-// Eight elements of the queries from element i on, as they are stored.
+// Eight elements of the queries from element i on: as they are stored, bf16 (P 1), or fp16 or fp32 (P 2).
 template <int P>
 __device__ __forceinline__ void load_q8(const AttnArgs& a, int64_t i, uint32_t (&w)[4 * P]) {
-    const uint8_t* p = static_cast<const uint8_t*>(a.q) + i * (2 * P);
+    const bool f32 = P == 2 && a.x_type == QMV_X_F32;
+    const uint8_t* p = static_cast<const uint8_t*>(a.q) + i * (f32 ? 4 : 2);
     if (a.qvec) {
 #pragma unroll
         for (int k = 0; k < P; ++k) {
+            if (k && !f32) continue;
             const u32x4 u = reinterpret_cast<const u32x4*>(p)[k];
 #pragma unroll
             for (int j = 0; j < 4; ++j) w[4 * k + j] = u[j];
         }
+    } else if (f32) {
+#pragma unroll
+        for (int j = 0; j < 4 * P; ++j) w[j] = reinterpret_cast<const uint32_t*>(p)[j];
     } else {
 #pragma unroll
-        for (int j = 0; j < 4 * P; ++j)
-            w[j] = P == 2 ? reinterpret_cast<const uint32_t*>(p)[j]
-                          : reinterpret_cast<const uint16_t*>(p)[2 * j] | (uint32_t)reinterpret_cast<const uint16_t*>(p)[2 * j + 1] << 16;
+        for (int j = 0; j < 4; ++j)
+            w[j] = reinterpret_cast<const uint16_t*>(p)[2 * j] | (uint32_t)reinterpret_cast<const uint16_t*>(p)[2 * j + 1] << 16;
     }
 }
 template <int P>
-__device__ __forceinline__ void widen_q8(const uint32_t (&w)[4 * P], bool f16, float (&x)[8]) {
-    if constexpr (P == 2) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = __builtin_bit_cast(float, w[j]);
-    } else if (f16) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            x[2 * j] = (float)as_h2(w[j])[0];
-            x[2 * j + 1] = (float)as_h2(w[j])[1];
-        }
-    } else {
+__device__ __forceinline__ void widen_q8(const AttnArgs& a, const uint32_t (&w)[4 * P], float (&x)[8]) {
+    if constexpr (P == 1) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             x[2 * j] = __builtin_bit_cast(float, w[j] << 16);
             x[2 * j + 1] = __builtin_bit_cast(float, w[j] & 0xffff0000u);
+        }
+    } else if (a.x_type == QMV_X_F32) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] = __builtin_bit_cast(float, w[j]);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            x[2 * j] = (float)as_h2(w[j])[0];
+            x[2 * j + 1] = (float)as_h2(w[j])[1];
         }
     }
 }
@@ -438,12 +445,15 @@ __device__ __forceinline__ f16x8 pack8(f16x2 a, f16x2 b, f16x2 c, f16x2 d) {
     return f16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
 
-// Waves per SIMD: what the accumulators and queries leave of the registers,
-// and the rings of LDS.
+// Waves per SIMD, and so workgroups per compute unit: what the accumulators and
+// queries leave of the registers, and the rings of LDS.  Three with small
+// heads (64 requests of 200..8000 tokens: 42 us, two 47), two with heads of
+// 128 (one request of 131000 tokens: 38 us, three 50, whose shares are smaller
+// and begin and end more often; 64 requests 65 and 70).
 template <int KF, int VF, int P, int NB, int NT>
 constexpr int stream_waves() {
     constexpr int lds = std::max(2 * Stage<KF, VF, NB>::kBytes, 16 * NT * 68 * 4) * kAWaves + 1024;
-    return std::min(P * NT * NB <= 4 ? 3 : P * NT * NB <= 8 ? 2 : 1, kLdsMax / lds);
+    return std::min(P * NT * NB <= 2 ? 3 : P * NT * NB <= 8 ? 2 : 1, kLdsMax / lds);
 }
 
 template <int KF, int VF, int P, int NB, int NT>
@@ -459,11 +469,11 @@ __global__ __launch_bounds__(kAT, (stream_waves<KF, VF, P, NB, NT>())) void attn
     const int n16 = lane & 15, g = lane >> 4;
     const float inf = __builtin_inff(), nan = __builtin_nanf("");
     // Codes of V are taken as fp16 kBase + c (8 bits: 1024 + 128 + c), with c or c - 8 the code.  Without minimums and with
-    // 16-bit queries the base goes with the scale, d (kBase + c) - d kBase in one multiply-add; d kBase is rounded, and what
+    // bf16 queries the base goes with the scale, d (kBase + c) - d kBase in one multiply-add; d kBase is rounded, and what
     // that adds to the sums is one product of the weights and the rounding errors, which are exact.  Where d kBase is no
     // number (|V| past 7000), the sums are not either and the careful pass takes the base off first.
     // K's codes go into the product as they are, the integers c 2^-24 that fp16 has below its normal numbers (odd pairs of
-    // 4-bit codes 16 times as large).  The matrix cores multiply those to about 2^-20: fp32 queries take them times 2^14.
+    // 4-bit codes 16 times as large).  The matrix cores multiply those to about 2^-20: with pairs of pieces they go in times 2^14.
     constexpr float kUnit = P == 2 ? 0x1p-10f : 0x1p-24f;
     constexpr bool kOffset = P == 1 && VF != QMV_Q4_1;
     constexpr float kBase = VF == QMV_Q8_0 ? 1152.f : VF == QMV_Q4_0 ? 72.f : 64.f;
@@ -601,7 +611,7 @@ __global__ __launch_bounds__(kAT, (stream_waves<KF, VF, P, NB, NT>())) void attn
             float w[NB][8];
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
-                widen_q8<P>(qw[nt][b], a.x_type == QMV_X_F16, w[b]);
+                widen_q8<P>(a, qw[nt][b], w[b]);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     amax = fmaxf(amax, __builtin_fabsf(w[b][j]));

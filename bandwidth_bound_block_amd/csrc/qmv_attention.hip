@@ -106,7 +106,7 @@ extern "C" int32_t qmv_cache_attention(const qmv_cache* cache, const void* q, in
     a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + round16((size_t)(n_requests + 2) * 8));
     const hipStream_t st = as_stream(stream);
     a.tile_part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + stream_bytes(*cache, n_requests, n_heads, max_q));
-    const bool two = x_type == QMV_X_F32;
+    const bool two = x_type != QMV_X_BF16;
     const int splits = tile_splits(*cache, n_tokens, n_heads, max_q, x_type);
     // of many requests some may be short; one that may be long goes the one way
     const bool both = splits > 0 && n_requests > 1;

@@ -1,4 +1,4 @@
-// The streaming attention kernel for Q4_0 keys and 16-bit queries.
+// The streaming attention kernel for Q4_0 keys and bf16 queries.
 #include "qmv_attention.h"
 
 namespace qmv {

@@ -1,4 +1,4 @@
-// The streaming attention kernel for Q4_1 keys and 16-bit queries.
+// The streaming attention kernel for Q4_1 keys and bf16 queries.
 #include "qmv_attention.h"
 
 namespace qmv {

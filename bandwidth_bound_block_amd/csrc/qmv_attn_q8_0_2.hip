@@ -1,4 +1,4 @@
-// The streaming attention kernel for Q8_0 keys and fp32 queries (two pieces).
+// The streaming attention kernel for Q8_0 keys and fp16 or fp32 queries (pairs of pieces).
 #include "qmv_attention.h"
 
 namespace qmv {

@@ -12,10 +12,13 @@
 // while one group multiplies (weights by values of a step, then queries by
 // keys of the next), the other does its softmax and turns codes into values,
 // the first group the keys', the second the values'.  All waves in step left
-// the matrix and the vector pipes waiting for each other: 458 us against ...
-// for 2048 queries behind 6144 keys, 32 heads.  Codes are on their way two
-// phases before they are used.  Few tiles are split over the keys and joined
-// by a second launch.
+// the matrix and the vector pipes waiting for each other: 458 us against 386
+// for 2048 bf16 queries behind 6144 keys, 32 heads of 128, Q4_0.  That is
+// 622 TF/s; what bounds it is the vector work beside the products (exponentials
+// and their scales, codes to values), about as long as they are.  Codes are on
+// their way two phases before they are used.  fp16 and fp32 queries (P 2) take
+// three products for one, 760..820 us.  Few tiles are split over the keys and
+// joined by a second launch.
 #pragma once
 #include "qmv_attention.h"
 
@@ -298,7 +301,7 @@ __global__ __launch_bounds__((Tile<D, P>::kThreads), (Tile<D, P>::kWaves / 4)) v
             for (int s = 0; s < D / 16; ++s) {
                 load_q8<P>(a, base + 16 * s + 8 * hh, w[s]);
                 float x[8];
-                widen_q8<P>(w[s], a.x_type == QMV_X_F16, x);
+                widen_q8<P>(a, w[s], x);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     amax = fmaxf(amax, __builtin_fabsf(x[j]));
@@ -313,7 +316,7 @@ __global__ __launch_bounds__((Tile<D, P>::kThreads), (Tile<D, P>::kWaves / 4)) v
 #pragma unroll
             for (int s = 0; s < D / 16; ++s) {
                 float x[8];
-                widen_q8<P>(w[s], a.x_type == QMV_X_F16, x);
+                widen_q8<P>(a, w[s], x);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     const float y = __builtin_ldexpf(x[j], sh);

@@ -1,4 +1,4 @@
-// The attention kernel for many rows of queries, 16-bit queries.
+// The attention kernel for many rows of queries, bf16 queries.
 #include "qmv_attn_tile.h"
 
 namespace qmv {

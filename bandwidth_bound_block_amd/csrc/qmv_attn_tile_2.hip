@@ -1,4 +1,4 @@
-// The attention kernel for many rows of queries, fp32 queries (two pieces).
+// The attention kernel for many rows of queries, fp16 or fp32 queries (pairs of pieces).
 #include "qmv_attn_tile.h"
 
 namespace qmv {
