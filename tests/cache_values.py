@@ -129,7 +129,7 @@ def attention(q, k, v, scale, pos, window, sink, x, few, k_fmt="q8_0"):
     out = w @ v
     # a score: products exact, up to 2 D + 64 roundings of partial sums and scales in fp32 (the queries' pieces: two of 2^-22
     # more); keys as fp16 values one of 2^-11 each; its multiple of log 2 and the difference to the maximum two more, and e^x 2^-22
-    two = x == "f32"
+    two = x != "bf16"
     es = (2 * D + 64 + (16 if two else 0)) * U * size + (0 if few or two else H16 * size) + (0 if few or not two else 8 * U * size)
     es = np.where(seen, es, 0.0)
     es = es + 4 * U * np.where(seen, np.abs(s), 0.0) + 4 * U * np.abs(top)[:, None] + 8 * U
