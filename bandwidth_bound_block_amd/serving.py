@@ -179,6 +179,8 @@ def qmv_cache_attention(cache, q, page_table, kv_lens, q_begin=None, max_q=None,
         if R < 1 or T % R or (max_q is not None and max_q * R != T):
             raise ValueError("without q_begin, every request has tokens / requests (max_q) queries")
         max_q = T // R
+    if not 0 <= window < 2 ** 31:
+        raise ValueError("window must be 0 (none) .. 2^31 - 1")
     sk = _pkg._full(sinks, "sinks", torch.float32, (heads,)) if sinks is not None else None
     if out is None:
         out = _pkg._new((T, heads, D), q.dtype, q, stream)
@@ -204,6 +206,8 @@ def qmv_logprobs(logits, targets=None, top_k=0, logprobs=None, entropy=None, top
     if logits.dim() != 2 or logits.stride(1) != 1:
         raise ValueError("logits must be [rows, vocab] with unit inner stride")
     N, V = logits.shape
+    if not 0 <= top_k <= 32:
+        raise ValueError("top_k must be 0..32")
     i32, f32 = torch.int32, torch.float32
     tp = lp = bt = bl = None
     n = 0

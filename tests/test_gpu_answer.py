@@ -78,3 +78,45 @@ def test_answers(monkeypatch):
     assert torch.equal(again[0], tokens)
     with pytest.raises(ValueError):
         ex.answer(model, ex.Attention(2, 1), prompts, n)
+
+
+def test_two_streams_at_once():
+    """The operators in a row on two streams, each with memory of its own, while the other's run: what each gives alone."""
+    import torch
+    import bandwidth_bound_block_amd as qmv
+    R, H, G, D, P, V = 9, 2, 4, 128, 16, 5000
+    g = torch.Generator(device="cuda").manual_seed(4)
+    lens = torch.tensor([1, 700, 33, 5, 2000, 64, 17, 300, 1200], dtype=torch.int32, device="cuda")
+    pages = 126
+    state = []
+    for i in range(2):
+        cache = qmv.KVCache.new(R * pages, "q8_0", "q4_1", H, D, P)
+        table = torch.randperm(R * pages, generator=g, device="cuda").to(torch.int32).view(R, pages)
+        at = [torch.arange(int(n), device="cuda") for n in lens]
+        slots = torch.cat([(table[r, a // P] * P + a % P).to(torch.int32) for r, a in enumerate(at)])
+        k, v = (torch.randn(slots.numel(), H, D, generator=g, device="cuda") for _ in range(2))
+        q = torch.randn(R, H * G, D, generator=g, device="cuda")
+        w = torch.randn(H * G * D, V, generator=g, device="cuda")
+        state.append((cache, k, v, slots, q, table, w))
+
+    def run(i, stream):
+        cache, k, v, slots, q, table, w = state[i]
+        qmv.qmv_cache_write(cache, k, v, slots, stream=stream)
+        a = qmv.qmv_cache_attention(cache, q, table, lens, stream=stream)
+        with torch.cuda.stream(stream):
+            l = a.view(R, -1) @ w
+        return (a,) + tuple(qmv.qmv_logprobs(l, None, top_k=7, stream=stream)[1:])
+    want = []
+    for i in range(2):
+        want.append([t.clone() for t in run(i, torch.cuda.current_stream())])
+        torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for c, *_ in state:
+        c.k.zero_()
+        c.v.zero_()
+    torch.cuda.synchronize()
+    for _ in range(5):
+        got = [run(i, streams[i]) for i in (0, 1)]
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert all(torch.equal(x, y) for x, y in zip(a, b))
