@@ -6,16 +6,16 @@
 // A = sum e^z (-z): sums of terms of one sign, so fp32 keeps the digits of a
 // row that is nearly certain.
 //
-// Two launches: every chunk of 4096 logits gives its maximum, T and A
+// Two launches: every chunk of 8192 logits gives its maximum, T and A
 // relative to it, and the maxima of groups of 64 logits; then a workgroup per
 // row joins the chunks.  Top tokens: the top_k-th largest of those maxima is
 // reached by the top_k most probable tokens, so only the few groups whose
 // maximum reaches it have candidates, whose logits the second launch reads
 // again; places among the candidates are counted.  Candidates found in the
 // first launch (ballots and a sort of lanes' maxima in every chunk) took 299
-// us for 500 x 151936, where the two launches now take 35 us (the read of the
-// logits, 4.4 TB/s) and 13 us (reads that wait for one another); one row of
-// 128256 takes 4 and 7 us.
+// us for 500 x 151936, where the two launches now take 31 us (152 MB at 4.9
+// TB/s, with 88% of the vector issue slots taken) and 13 us (reads
+// that wait for one another); one row of 128256 takes 4.5 and 7 us.
 #include <algorithm>
 #include <type_traits>
 
@@ -29,10 +29,10 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kLT = 256;
 constexpr int kLWaves = kLT / 64;
-// Logits of a thread: with 64 the first launch took 5.9 us for one row of
-// 128256, with 16 it takes 4.0; 500 rows of 151936 take 50.4 us with 64 and
-// 48.8 with 16, both launches.
-constexpr int kLPer = 16;
+// Logits of a thread: the first launch takes 30.7 us for 500 rows of 151936
+// bf16 logits, with 16 a thread 32.6; for one row of 128256 4.5 and 3.9, with
+// 64 it was 5.9.
+constexpr int kLPer = 32;
 constexpr int kLGroup = 64;                   // logits of a group: those of kLGroup / kLPer threads
 constexpr int kLTop = 32;
 constexpr int kLCands = 1024;                 // groups that reach the bound, and candidates, of a row that LDS holds
@@ -76,15 +76,29 @@ __device__ __forceinline__ float exp_neg32(float z) {
 // The larger one, NaN if either is.
 __device__ __forceinline__ float max_or_nan(float a, float b) { return __builtin_elementwise_maximum(a, b); }
 
+// A value over all lanes: neighbours, quads, eights, rows of 16 by moves within a row of lanes, then rows and halves.  By
+// way of LDS (__shfl_xor) these steps were a quarter of the first launch's instructions.
+template <class Op>
+__device__ __forceinline__ float over_wave(float v, const Op& op) {
+    const auto moved = [](float x, auto how) {
+        return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, x), decltype(how)::value, 0xf, 0xf, true));
+    };
+    v = op(v, moved(v, std::integral_constant<int, 0xb1>{}));      // lane ^ 1
+    v = op(v, moved(v, std::integral_constant<int, 0x4e>{}));      // lane ^ 2
+    v = op(v, moved(v, std::integral_constant<int, 0x141>{}));     // mirrored within 8
+    v = op(v, moved(v, std::integral_constant<int, 0x140>{}));     // mirrored within 16
+    const uint32_t a = __builtin_bit_cast(uint32_t, v);
+    const auto r = __builtin_amdgcn_permlane16_swap(a, a, false, false);
+    v = op(__builtin_bit_cast(float, (uint32_t)r[0]), __builtin_bit_cast(float, (uint32_t)r[1]));
+    const uint32_t b = __builtin_bit_cast(uint32_t, v);
+    const auto h = __builtin_amdgcn_permlane32_swap(b, b, false, false);
+    return op(__builtin_bit_cast(float, (uint32_t)h[0]), __builtin_bit_cast(float, (uint32_t)h[1]));
+}
 __device__ __forceinline__ float wave_sum(float s) {
-#pragma unroll
-    for (int o = 32; o; o >>= 1) s += __shfl_xor(s, o);
-    return s;
+    return over_wave(s, [](float a, float b) { return a + b; });
 }
 __device__ __forceinline__ float wave_max(float m) {
-#pragma unroll
-    for (int o = 32; o; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
-    return m;
+    return over_wave(m, [](float a, float b) { return fmaxf(a, b); });
 }
 // A number that grows with x, and for equal x with a smaller id; +0 and -0 are equal.
 __device__ __forceinline__ uint64_t order_key(float x, int id) {
@@ -167,26 +181,25 @@ __global__ __launch_bounds__(kLT) void logprobs_chunk_kernel(const LogprobArgs a
             for (int o = 1; o < kThreads; o <<= 1) g = fmaxf(g, __shfl_xor(g, o));
             if (threadIdx.x % kThreads == 0) a.most[at * (kLT / kThreads) + threadIdx.x / kThreads] = g;
         }
-        float m = mine;
-#pragma unroll
-        for (int o = 32; o; o >>= 1) m = max_or_nan(m, __shfl_xor(m, o));
+        float m = over_wave(mine, max_or_nan);
         __syncthreads();          // the last row's reads
         if (lane == 0) wm[wave] = m;
         __syncthreads();
         m = max_or_nan(max_or_nan(wm[0], wm[1]), max_or_nan(wm[2], wm[3]));
         // largest terms are 1 each and are counted: beside them the small ones would lose their digits
         float t = 0.f, e_a = 0.f;
-        int tops = 0;
+        float count = 0.f;
         const bool good = m > -inf && m < inf;
         if (good && __any(mine == m)) {
 #pragma unroll
             for (int i = 0; i < kLPer; ++i) {
                 const float z = fmaxf(f[i] - m, -1000.f), e = __builtin_amdgcn_exp2f(z * 1.44269504088896341f);
                 const bool top = z == 0.f;
-                tops += top;
+                count += top ? 1.f : 0.f;
                 t += top ? 0.f : e;
                 e_a = __builtin_fmaf(e, -z, e_a);
             }
+            count = wave_sum(count);
         } else if (good) {        // most waves: what is left out here was a third of the launch's instructions
 #pragma unroll
             for (int i = 0; i < kLPer; ++i) {
@@ -197,7 +210,6 @@ __global__ __launch_bounds__(kLT) void logprobs_chunk_kernel(const LogprobArgs a
         }
         t = wave_sum(t);
         e_a = wave_sum(e_a);
-        const float count = wave_sum((float)tops);
         if (lane == 0) {
             wt[wave] = t;
             wa[wave] = e_a;

@@ -745,7 +745,8 @@ int32_t qmv_cache_attention(const qmv_cache* cache, const void* q, int32_t x_typ
  *   entropy   fp32 [n_rows], or null.
  *   top_k     0..32 (0: top_tokens and top_logprobs may be null).  Where fewer
  *             tokens have a probability, the rest are token -1 at -inf.
- *   n_rows 1..2^20, vocab 1..2^22, n_rows * vocab chunks of 4096 below 2^28.
+ *   n_rows 1..2^20, vocab 1..2^22, n_rows times the chunks of 8192
+ *             of vocab below 2^28.
  *   workspace device memory of >= qmv_logprobs_workspace_bytes(...) bytes,
  *             16-byte aligned; any contents; calls that share one must not
  *             run concurrently (values pass between launches in it).
