@@ -59,7 +59,7 @@ def cache_page_bytes(fmt, n_kv_heads, head_dim, page_size):
 class KVCache:
     """The pages of a cache: uint8 GPU tensors k and v of whole pages, their
     formats, and the sizes that make a page.  The memory is the caller's and
-    may hold anything where no token was written."""
+    may hold anything where no token was written.  The attributes are fixed."""
     __slots__ = ("k", "v", "k_fmt", "v_fmt", "n_kv_heads", "head_dim", "page_size", "n_pages", "_struct")
 
     def __init__(self, k, v, k_fmt, v_fmt, n_kv_heads, head_dim, page_size):
@@ -73,6 +73,11 @@ class KVCache:
         self.k, self.v, self.k_fmt, self.v_fmt = k, v, _pkg._fmt(k_fmt), _pkg._fmt(v_fmt)
         self.n_kv_heads, self.head_dim, self.page_size, self.n_pages = n_kv_heads, head_dim, page_size, n
         self._struct = CacheStruct(kp, vp, n, self.k_fmt, self.v_fmt, n_kv_heads, head_dim, page_size, 0)
+
+    def __setattr__(self, name, value):
+        if hasattr(self, "_struct"):      # set last: it has the pages' addresses
+            raise AttributeError("a cache's pages and sizes are fixed")
+        object.__setattr__(self, name, value)
 
     @classmethod
     def new(cls, n_pages, k_fmt, v_fmt, n_kv_heads, head_dim, page_size, device="cuda"):

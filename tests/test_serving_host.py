@@ -99,6 +99,16 @@ def test_calls_on_another_gpu_than_the_current_one(stand):
         qmv.qmv_logprobs(gpu(3, 9), elsewhere(ids(3)))
 
 
+def test_a_cache_is_fixed(stand):
+    """The library is given addresses: other pages are another cache."""
+    _, qmv = stand
+    c = cache(qmv)
+    for name in ("k", "v", "n_pages", "k_fmt", "page_size"):
+        with pytest.raises(AttributeError):
+            setattr(c, name, getattr(c, name))
+    assert c.n_pages == 3 and (c.k_fmt, c.v_fmt) == (qmv.Q8_0, qmv.Q4_0)
+
+
 REFUSED = [
     lambda q: q.KVCache(raw(200), raw(192), "q8_0", "q4_0", 2, 64, 16),                     # no whole pages
     lambda q: q.KVCache(raw(128), raw(192), "q8_0", "q4_0", 2, 64, 16),
