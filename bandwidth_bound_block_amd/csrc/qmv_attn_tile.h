@@ -14,7 +14,7 @@
 // the first group the keys', the second the values'.  All waves in step left
 // the matrix and the vector pipes waiting for each other: 458 us against 386
 // for 2048 bf16 queries behind 6144 keys, 32 heads of 128, Q4_0.  That is
-// 622 TF/s; what bounds it is the vector work beside the products (exponentials
+// 622 TF/s (324 us, 742, where calls follow each other); what bounds it is the vector work beside the products (exponentials
 // and their scales, codes to values), about as long as they are.  Codes are on
 // their way two phases before they are used.  fp16 and fp32 queries (P 2) take
 // three products for one, 760..820 us.  Few tiles are split over the keys and
