@@ -15,7 +15,7 @@
 // and values are rounded to fp16 (2^-11; the outputs to 2^-8).  With fp16 or
 // fp32 queries they are pairs of fp16 pieces, fp32 queries too: fp16 outputs
 // had twice the error of their own rounding without.  That costs little here
-// (131000 tokens: 44 us) and twice the time where arithmetic is the bound.
+// (131000 tokens: 41 us) and twice the time where arithmetic is the bound.
 //
 // The transposition that V needs (a lane multiplies eight keys of one place of
 // the head) happens inside the lane: it loads the same few values of its eight
