@@ -91,6 +91,12 @@ int32_t attn_tile_2(const AttnArgs& a, int D, int splits, hipStream_t st);
 namespace {
 
 constexpr float kANone = -1e30f;    // the maximum of no score
+// The running maximum is kept this much lower than the largest score, in units
+// of log 2: weights go up to 2^14 (fp16 holds 65504), so that those far below
+// the largest keep their digits.  As numbers of up to 1 they were 0 from 2^-25
+// on, and beside one key with nearly all the weight and no value the output was
+// lost (18 nats under it: two thirds); now from 2^-39 on, 27 nats.
+constexpr float kALow = 14.f;
 
 struct Req {
     int64_t q0;                     // first query token
@@ -811,13 +817,13 @@ __global__ __launch_bounds__(kAT, (stream_waves<KF, VF, P, NB, NT>())) void attn
                             }
                         }
                     }
-                    // softmax: running maximum and sum, in units of log 2
+                    // softmax: running maximum (kALow under it) and sum, in units of log 2
                     f16x8 ph[NT], pl[NT];
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
                         float top = fmaxf(fmaxf(fmaxf(s[nt][0][0], s[nt][0][1]), fmaxf(s[nt][0][2], s[nt][0][3])),
                                           fmaxf(fmaxf(s[nt][1][0], s[nt][1][1]), fmaxf(s[nt][1][2], s[nt][1][3])));
-                        top = fmaxf(groups_max(top * fac[nt]), m[nt]);
+                        top = fmaxf(groups_max(__builtin_fmaf(top, fac[nt], -kALow)), m[nt]);
                         if (__any(top > m[nt])) {
                             const float f = __builtin_amdgcn_exp2f(m[nt] - top);
                             l[nt] *= f;
@@ -833,11 +839,17 @@ __global__ __launch_bounds__(kAT, (stream_waves<KF, VF, P, NB, NT>())) void attn
 #pragma unroll
                             for (int i = 0; i < 4; ++i) {
                                 const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(s[nt][t][i], fac[nt], -m[nt]));
-                                l[nt] += p;
                                 const _Float16 hi = (_Float16)p;
                                 ph[nt][4 * t + i] = hi;
-                                if constexpr (P == 2) pl[nt][4 * t + i] = (_Float16)(p - (float)hi);
+                                if constexpr (P == 2) {
+                                    l[nt] += p;
+                                    pl[nt][4 * t + i] = (_Float16)(p - (float)hi);
+                                }
                             }
+                        if constexpr (P == 1)      // the sum of the weights as they are multiplied
+#pragma unroll
+                            for (int i = 0; i < 8; i += 2)
+                                l[nt] = __builtin_amdgcn_fdot2(f16x2{ph[nt][i], ph[nt][i + 1]}, h2(1.f), l[nt], false);
                     }
                     // values: tile v of the result's places, keys in the order of the weights
                     f16x2 vd[4][S::kVB], ve[4][S::kVB];      // pairs of keys 2 j, 2 j + 1: scales, and minimums or offsets

@@ -475,7 +475,7 @@ __global__ __launch_bounds__((Tile<D, P>::kThreads), (Tile<D, P>::kWaves / 4)) v
                 for (int t = 0; t < NT; ++t)
 #pragma unroll
                     for (int i = 0; i < 16; ++i) top = fmaxf(top, s[t][i]);
-                const uint32_t tw = __builtin_bit_cast(uint32_t, top * fac);
+                const uint32_t tw = __builtin_bit_cast(uint32_t, __builtin_fmaf(top, fac, -kALow));
                 const auto x = __builtin_amdgcn_permlane32_swap(tw, tw, false, false);
                 top = fmaxf(fmaxf(__builtin_bit_cast(float, (uint32_t)x[0]), __builtin_bit_cast(float, (uint32_t)x[1])), m);
                 if (__any(top > m)) {
