@@ -100,7 +100,7 @@ constexpr float kALow = 14.f;
 
 struct Req {
     int64_t q0;                     // first query token
-    int n, len;                     // query tokens, keys
+    int n, len;                     // query tokens (max_q at most), keys up to the last one's
     int lo, blk0, nblk;             // first key seen, first block, blocks of a unit
     int tiles;                      // tiles of rows
     __device__ int cost() const { return nblk + kABegin; }
@@ -121,7 +121,8 @@ __device__ __forceinline__ Req request(const AttnArgs& a, int r) {
     o.n = (int)min(e - b, a.max_q);
     const int len = a.lens[r];
     o.bad = len < 0 || len > (a.max_pages << a.page_shift);
-    o.len = o.bad ? 0 : len;
+    // queries past max_q are left out with their own keys, which no other query sees: the others stand where they stood
+    o.len = o.bad ? 0 : (int)(len - (e - b - o.n));
     o.lo = a.window > 0 ? (int)max((int64_t)0, (int64_t)o.len - o.n - a.window + 1) : 0;
     o.blk0 = o.lo / kABlock;
     o.nblk = max(1, (int)(((int64_t)o.len + kABlock - 1) / kABlock) - o.blk0);

@@ -161,7 +161,7 @@ def qmv_cache_attention(cache, q, page_table, kv_lens, q_begin=None, max_q=None,
     int32 [requests, max_pages]; kv_lens int32 [requests], the new tokens
     counted in; q_begin int32 [requests + 1]: request r's queries are tokens
     q_begin[r] .. q_begin[r + 1] - 1, of which it may have max_q (an int, the
-    most of any request; all tokens by default).  Without q_begin every
+    most of any request; all tokens by default; those past it are left out).  Without q_begin every
     request has tokens / requests of them.  scale: 1 / sqrt(head_dim) by
     default; window 0: none; sinks float32 [heads] or None.  Returns out
     [tokens, heads, head_dim] of q's type; rows of no request are not

@@ -700,7 +700,8 @@ int32_t qmv_cache_read(const qmv_cache* cache, const int32_t* slots, int64_t n_t
  *              and n_tokens = n_requests * max_q.  All of these are device
  *              memory.
  *   max_q      the most query tokens of a request, 1..n_tokens; of a request
- *              that has more, those past max_q are left out.
+ *              that has more, those past max_q are left out (n counts them:
+ *              the others stand where they would stand with them).
  *   scale      finite, > 0;  window 0 (none) or > 0;  sinks fp32 [n_heads]
  *              or null.
  *   out        x_type [n_tokens][n_heads][head_dim], contiguous.  Rows of no
