@@ -97,6 +97,15 @@ constexpr float kANone = -1e30f;    // the maximum of no score
 // on, and beside one key with nearly all the weight and no value the output was
 // lost (18 nats under it: two thirds); now from 2^-39 on, 27 nats.
 constexpr float kALow = 14.f;
+// Scores (times log2 e) from which on fp32 has no halves: a score's product
+// and its maximum, rounded, may differ by any power of two, so that weights
+// are infinite or all 0.  A part whose maximum is that far from 0 is done
+// again in the careful pass, where both are rounded alike before their
+// difference, which is 0 for the largest, and the maximum is kept as it is.
+// (Looked for in every step it costs 1% to 4%.)
+constexpr float kAFar = 0x1p24f;
+__device__ __forceinline__ float lowered(float most) { return most - (__builtin_fabsf(most) < kAFar ? kALow : 0.f); }
+__device__ __forceinline__ bool is_far(float m) { return __builtin_fabsf(m) >= kAFar && m > kANone; }
 
 struct Req {
     int64_t q0;                     // first query token
@@ -651,7 +660,7 @@ __global__ __launch_bounds__(kAT, (stream_waves<KF, VF, P, NB, NT>())) void attn
 
         float m[NT], l[NT];
         f32x4 o[NT][NV];
-        // All of the wave's blocks; `care`: with values that are not finite by themselves.
+        // All of the wave's blocks; `care`: with values that are not finite by themselves, and scores far from 0.
         const auto pass = [&](auto care) {
             constexpr bool careful = decltype(care)::value, offset = kOffset && !careful;
             f32x4 poison[NT][S::kVB], corr[NT][S::kVB];
@@ -824,7 +833,8 @@ __global__ __launch_bounds__(kAT, (stream_waves<KF, VF, P, NB, NT>())) void attn
                     for (int nt = 0; nt < NT; ++nt) {
                         float top = fmaxf(fmaxf(fmaxf(s[nt][0][0], s[nt][0][1]), fmaxf(s[nt][0][2], s[nt][0][3])),
                                           fmaxf(fmaxf(s[nt][1][0], s[nt][1][1]), fmaxf(s[nt][1][2], s[nt][1][3])));
-                        top = fmaxf(groups_max(__builtin_fmaf(top, fac[nt], -kALow)), m[nt]);
+                        if constexpr (careful) top = fmaxf(lowered(groups_max(top * fac[nt])), m[nt]);
+                        else top = fmaxf(groups_max(__builtin_fmaf(top, fac[nt], -kALow)), m[nt]);
                         if (__any(top > m[nt])) {
                             const float f = __builtin_amdgcn_exp2f(m[nt] - top);
                             l[nt] *= f;
@@ -835,11 +845,20 @@ __global__ __launch_bounds__(kAT, (stream_waves<KF, VF, P, NB, NT>())) void attn
                                 for (int k = 0; k < S::kVB; ++k) corr[nt][k] *= f;
                             m[nt] = top;
                         }
+                        float unit = fac[nt];
+                        if constexpr (careful) {
+                            const bool far = is_far(m[nt]);
+#pragma unroll
+                            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) s[nt][t][i] *= far ? unit : 1.f;
+                            unit = far ? 1.f : unit;
+                        }
 #pragma unroll
                         for (int t = 0; t < 2; ++t)
 #pragma unroll
                             for (int i = 0; i < 4; ++i) {
-                                const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(s[nt][t][i], fac[nt], -m[nt]));
+                                const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(s[nt][t][i], unit, -m[nt]));
                                 const _Float16 hi = (_Float16)p;
                                 ph[nt][4 * t + i] = hi;
                                 if constexpr (P == 2) {
@@ -930,12 +949,15 @@ __global__ __launch_bounds__(kAT, (stream_waves<KF, VF, P, NB, NT>())) void attn
         pass(std::false_type{});
         bool odd = false;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int nt = 0; nt < NT; ++nt) {
+            odd |= is_far(m[nt]);
 #pragma unroll
             for (int v = 0; v < NV; ++v)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) odd |= !(__builtin_fabsf(o[nt][v][i]) < inf);
-        // 0 times a value that is not finite, of a key that a row does not see: again, with such values by themselves
+        }
+        // 0 times a value that is not finite, of a key that a row does not see: again, with such values by themselves.  Scores
+        // that were far from 0 before the maximum came near it: their weights, infinite or not, were multiplied by 0 there
         if (__builtin_expect(__any(odd), 0)) pass(std::true_type{});
 
         // ---- the waves' parts meet

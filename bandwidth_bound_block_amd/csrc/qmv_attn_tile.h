@@ -345,7 +345,7 @@ __global__ __launch_bounds__((Tile<D, P>::kThreads), (Tile<D, P>::kWaves / 4)) v
         float m, l;
         f32x16 o[NB];
         // All of the split's blocks, by the first group (Raw: keys) and by the second (values); `care`: with values that are
-        // not finite by themselves.
+        // not finite by themselves, and scores far from 0.
         const auto pass = [&](auto care, auto raw) {
             constexpr bool careful = decltype(care)::value;
             typedef decltype(raw) Raw;
@@ -475,9 +475,10 @@ __global__ __launch_bounds__((Tile<D, P>::kThreads), (Tile<D, P>::kWaves / 4)) v
                 for (int t = 0; t < NT; ++t)
 #pragma unroll
                     for (int i = 0; i < 16; ++i) top = fmaxf(top, s[t][i]);
-                const uint32_t tw = __builtin_bit_cast(uint32_t, __builtin_fmaf(top, fac, -kALow));
+                const uint32_t tw = __builtin_bit_cast(uint32_t, careful ? top * fac : __builtin_fmaf(top, fac, -kALow));
                 const auto x = __builtin_amdgcn_permlane32_swap(tw, tw, false, false);
-                top = fmaxf(fmaxf(__builtin_bit_cast(float, (uint32_t)x[0]), __builtin_bit_cast(float, (uint32_t)x[1])), m);
+                top = fmaxf(__builtin_bit_cast(float, (uint32_t)x[0]), __builtin_bit_cast(float, (uint32_t)x[1]));
+                top = fmaxf(careful ? lowered(top) : top, m);
                 if (__any(top > m)) {
                     const float f = __builtin_amdgcn_exp2f(m - top);
                     l *= f;
@@ -485,13 +486,22 @@ __global__ __launch_bounds__((Tile<D, P>::kThreads), (Tile<D, P>::kWaves / 4)) v
                     for (int v = 0; v < NB; ++v) o[v] *= f;
                     m = top;
                 }
+                float unit = fac;
+                if constexpr (careful) {
+                    const bool far = is_far(m);
+#pragma unroll
+                    for (int t = 0; t < NT; ++t)
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) s[t][i] *= far ? unit : 1.f;
+                    unit = far ? 1.f : unit;
+                }
 #pragma unroll
                 for (int t = 0; t < NT; ++t)
 #pragma unroll
                     for (int u = 0; u < 2; ++u) {
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
-                            const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][8 * u + i], fac, -m));
+                            const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][8 * u + i], unit, -m));
                             const _Float16 hi = (_Float16)p;
                             ph[t][u][i] = hi;
                             if constexpr (P == 2) {
@@ -550,12 +560,12 @@ __global__ __launch_bounds__((Tile<D, P>::kThreads), (Tile<D, P>::kWaves / 4)) v
         };
         if (second) pass(std::false_type{}, RawV<D, P, V8>());
         else pass(std::false_type{}, RawK<D, P, K8>());
-        bool odd = false;
+        bool odd = is_far(m);
 #pragma unroll
         for (int v = 0; v < NB; ++v)
 #pragma unroll
             for (int i = 0; i < 16; ++i) odd |= !(__builtin_fabsf(o[v][i]) < inf);
-        // 0 times a value that is not finite, of a key that a row does not see: again, with such values by themselves
+        // 0 times a value that is not finite, of a key that a row does not see, or scores far from 0: again, with care
         if (__builtin_expect(__syncthreads_or(odd), 0)) {
             if (second) pass(std::true_type{}, RawV<D, P, V8>());
             else pass(std::true_type{}, RawK<D, P, K8>());
