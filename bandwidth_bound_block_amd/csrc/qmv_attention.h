@@ -59,7 +59,7 @@ struct AttnArgs {
     int64_t max_pages;
     const int32_t* lens;
     const int32_t* q_begin;
-    float scale;                    // times log2(e)
+    float scale;
     int32_t window;
     const float* sinks;
     void* out;
@@ -90,7 +90,7 @@ int32_t attn_tile_2(const AttnArgs& a, int D, int splits, hipStream_t st);
 
 namespace {
 
-constexpr float kANone = -1e30f;    // the maximum of no score
+constexpr float kANone = -0x1p127f; // the maximum of no score: scores are less than 2^126 either way
 // The running maximum is kept this much lower than the largest score, in units
 // of log 2: weights go up to 2^14 (fp16 holds 65504), so that those far below
 // the largest keep their digits.  As numbers of up to 1 they were 0 from 2^-25
@@ -294,10 +294,17 @@ __device__ __forceinline__ void finish(const AttnArgs& a, int hq, float m, float
 }
 
 // A row's power of two: |q| 2^shift < 2^15 throughout.  A row that is not
-// finite gives NaN.  At most 2^60: scores of smaller rows are 0 to fp32 beside
-// any others.
+// finite gives NaN.
 __device__ __forceinline__ int row_shift(float amax) {
-    return amax > 0.f ? min(14 - (int)((__builtin_bit_cast(uint32_t, amax) >> 23) & 255) + 127, 60) : 0;
+    return amax > 0.f ? 14 - (int)((__builtin_bit_cast(uint32_t, amax) >> 23) & 255) + 127 : 0;
+}
+// What sums over a row of queries times 2^shift, in units of 2^unit, are
+// multiplied by: the rest of the scale, for scores in units of log 2.  Not 0, as what is out of sight is -inf times it.  Sums are
+// less than 2^15 * 65024 * 256 units (< 2^39): up to 2^87 scores stay within
+// fp32, and more would change nothing (two sums are a unit's 2^-48 apart at
+// least, or alike).
+__device__ __forceinline__ float row_factor(const AttnArgs& a, int shift, int unit) {
+    return fminf(fmaxf(__builtin_ldexpf(a.scale, -shift - unit) * 1.44269504088896341f, 1e-37f), __builtin_ldexpf(1.f, 87 - unit));
 }
 
 constexpr int row_bytes_of(int F, int D) { return F == QMV_Q8_0 ? D : D / 2; }
@@ -490,6 +497,7 @@ __global__ __launch_bounds__(kAT, (stream_waves<KF, VF, P, NB, NT>())) void attn
     // number (|V| past 7000), the sums are not either and the careful pass takes the base off first.
     // K's codes go into the product as they are, the integers c 2^-24 that fp16 has below its normal numbers (odd pairs of
     // 4-bit codes 16 times as large).  The matrix cores multiply those to about 2^-20: with pairs of pieces they go in times 2^14.
+    constexpr int kUnitLog = P == 2 ? -10 : -24;
     constexpr float kUnit = P == 2 ? 0x1p-10f : 0x1p-24f;
     constexpr bool kOffset = P == 1 && VF != QMV_Q4_1;
     constexpr float kBase = VF == QMV_Q8_0 ? 1152.f : VF == QMV_Q4_0 ? 72.f : 64.f;
@@ -636,7 +644,7 @@ __global__ __launch_bounds__(kAT, (stream_waves<KF, VF, P, NB, NT>())) void attn
             }
             amax = groups_max(amax);
             const int sh = row_shift(amax);
-            fac[nt] = fmaxf(__builtin_ldexpf(a.scale / kUnit, -sh), 1e-37f);      // not 0: what is out of sight is -inf times it
+            fac[nt] = row_factor(a, sh, kUnitLog);
             if (groups_max(fin ? 0.f : 1.f) != 0.f) fac[nt] = __builtin_nanf("");
 #pragma unroll
             for (int b = 0; b < NB; ++b) {

@@ -97,7 +97,7 @@ extern "C" int32_t qmv_cache_attention(const qmv_cache* cache, const void* q, in
     a.max_pages = max_pages;
     a.lens = kv_lens;
     a.q_begin = q_begin;
-    a.scale = scale * 1.44269504088896341f;
+    a.scale = scale;
     a.window = window > (1 << 30) ? 1 << 30 : window;
     a.sinks = sinks;
     a.out = out;

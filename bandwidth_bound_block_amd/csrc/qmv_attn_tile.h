@@ -316,7 +316,7 @@ __global__ __launch_bounds__((Tile<D, P>::kThreads), (Tile<D, P>::kWaves / 4)) v
             }
             amax = fmaxf(amax, __shfl_xor(amax, 32));
             const int sh = row_shift(amax);
-            fac = fmaxf(__builtin_ldexpf(a.scale, -sh), 1e-37f);
+            fac = row_factor(a, sh, 0);
             const int odd = fin ? 0 : 1;
             if (odd | __shfl_xor(odd, 32)) fac = nan;
 #pragma unroll

@@ -715,13 +715,13 @@ int32_t qmv_cache_read(const qmv_cache* cache, const int32_t* slots, int64_t n_t
  * other lengths, tables and q_begin (within max_q).
  * Statistics and sums are fp32.  bf16 queries: codes are exact in the matrix
  * cores' fp16, queries are scaled by a power of two per row to fp16 (exact
- * for all elements within 2^-28 of the row's largest), weights and DEQ(V) are
+ * for all elements within 2^-27 of the row's largest), weights and DEQ(V) are
  * rounded to fp16, and so is DEQ(K) for a request, or a call of one request,
  * that may have more than 32 rows of queries (query tokens times n_heads /
  * n_kv_heads).  fp16 and fp32 queries: two fp16 pieces of each, 22 bits, at
  * twice the arithmetic.  A weight is off by that relative to itself, and by
- * 2^-39 of the row's largest (those 27 nats under it are 0).  |DEQ(V)| must be
- * within fp16's range, as qmv_cache_write has it.  A NaN in the cache reaches the queries
+ * 2^-39 of the row's largest (those 27 nats under it are 0).  |DEQ(K)|
+ * and |DEQ(V)| must be within 65024, as qmv_cache_write has them.  A NaN in the cache reaches the queries
  * that see it and no others.  The same call gives the same bits; the other
  * requests' lengths can change the order of a query's sums, nothing else.
  * Errors: QMV_EINVAL, QMV_EALIGN, QMV_EUNSUPPORTED (format), QMV_EHIP.

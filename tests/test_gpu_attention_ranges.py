@@ -53,3 +53,58 @@ def test_scores_past_24_bits(env, x, new, size):
     # four weights of a quarter, their quotient and sums: a few roundings; each value's own, as above; the output's
     bound = mean * ((ab.H16 * 3 if x == "bf16" else 0) + 32 * ab.U) * 1.01 + 2.0 ** -25
     ab.close(got, want, bound + ab.HALF[x] * (want.abs() + bound))
+
+
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("size", [1e12, 1e25, 1e30, 1e34, 1e37, 3e38])
+@pytest.mark.parametrize("kf", ["q8_0", "q4_0", "q4_1"])
+@pytest.mark.parametrize("new", [2, 45])
+@pytest.mark.parametrize("x", ["f32", "bf16"])
+def test_large_queries(env, x, new, kf, size, sign):
+    """All of the weight is on the key with the largest score, also where all scores are far below zero or past fp32."""
+    torch, qmv = env
+    print(x, new, kf, size, sign, flush=True)
+    H, G, D, L, best = 2, 2, 128, 333, 77
+    g = torch.Generator(device="cuda").manual_seed(1)
+    u = torch.sign(torch.randn(H, D, generator=g, device="cuda"))
+    # scores sign * c: the largest is c = 2 of 0.5..1.5, or 0.5 of 1..2
+    c = 0.5 + torch.rand(L, generator=g, device="cuda")
+    c[best] = 2.0
+    c = sign * (c if sign > 0 else c + 0.5)
+    if sign < 0:
+        c[best] = -0.5
+    v = torch.randn(L, H, D, generator=g, device="cuda")
+    cache, table = filled(torch, qmv, c[:, None, None] * u, v, kf, "q8_0")
+    q = (size * u.repeat_interleave(G, 0)).expand(new, -1, -1).to(getattr(torch, TYPES[x])).contiguous()
+    assert bool(torch.isfinite(q.float()).all())
+    # read back the order holds, by more than a score's rounding
+    s = torch.einsum("lhd,hd->lh", qmv.qmv_cache_read(cache, torch.arange(cache.n_pages * 16, dtype=torch.int32, device="cuda"))[0][
+        (table[0].long()[:, None] * 16 + torch.arange(16, device="cuda")).flatten()[:L]].double(), u.double())
+    two = s.topk(2, dim=0)
+    assert bool((two.indices[0] == best).all()) and bool((two.values[0] - two.values[1] > 0.05 * s.abs().amax(0)).all())
+    got = qmv.qmv_cache_attention(cache, q, table.contiguous(), torch.tensor([L], dtype=torch.int32, device="cuda"))
+    at = (table[0, best // 16] * 16 + best % 16).to(torch.int32).view(1)
+    want = qmv.qmv_cache_read(cache, at)[1].double().repeat_interleave(G, 1).expand(new, -1, -1)
+    seen = torch.arange(L - new, L, device="cuda") >= best
+    assert bool(seen.all())
+    # weight 1 and the value as fp16 (beside an offset's rounding, half a scale at most) or two pieces, the output rounded
+    half = ab.HALF[x] + (2 * ab.H16 if x == "bf16" else 8 * ab.U)
+    ab.close(got, want, want.abs() * half * 1.01 + 2.0 ** -25)
+
+
+@pytest.mark.parametrize("power", [20, 60, 100, 120])
+@pytest.mark.parametrize("new", [2, 45])
+@pytest.mark.parametrize("x", ["f32", "bf16"])
+def test_small_queries_with_a_large_scale(env, x, new, power):
+    """Powers of two moved from the queries to the scale change nothing."""
+    torch, qmv = env
+    print(x, new, power, flush=True)
+    H, G, D, L = 2, 2, 128, 200
+    g = torch.Generator(device="cuda").manual_seed(2)
+    k, v = (torch.randn(L, H, D, generator=g, device="cuda") for _ in range(2))
+    cache, table = filled(torch, qmv, k, v, "q8_0", "q4_0")
+    q = torch.randn(new, H * G, D, generator=g, device="cuda").to(getattr(torch, TYPES[x]))
+    q = torch.where(q.abs() < 2.0 ** -5, torch.zeros_like(q), q)      # no element is below the type's normal numbers
+    n = torch.tensor([L], dtype=torch.int32, device="cuda")
+    got = qmv.qmv_cache_attention(cache, q * 2.0 ** -power, table, n, scale=2.0 ** power * D ** -0.5)
+    ab.close(got, *ab.of_cache(qmv, cache, q, table, [L], [0, new], D ** -0.5, x))
