@@ -280,10 +280,16 @@ __device__ __forceinline__ void store_out4(const AttnArgs& a, int64_t i, f32x4 x
     }
 }
 
+// A sink's logit in units of log 2.  Past fp32 it is its largest number, which
+// no score comes near: the difference of two infinities would be NaN.
+__device__ __forceinline__ float sink_of(const AttnArgs& a, int hq) {
+    const float sk = a.sinks[hq] * 1.44269504088896341f;
+    return sk > 0x1.fffffep127f ? 0x1.fffffep127f : sk;
+}
 // Sums x and l relative to the maximum m, of query head hq, to outputs.
 __device__ __forceinline__ void finish(const AttnArgs& a, int hq, float m, float l, f32x4& x, bool bad) {
     if (a.sinks) {
-        const float sk = a.sinks[hq] * 1.44269504088896341f, top = fmaxf(m, sk);
+        const float sk = sink_of(a, hq), top = fmaxf(m, sk);
         const float f = __builtin_amdgcn_exp2f(m - top);
         x *= f;
         l = l * f + __builtin_amdgcn_exp2f(sk - top);

@@ -577,7 +577,7 @@ __global__ __launch_bounds__((Tile<D, P>::kThreads), (Tile<D, P>::kWaves / 4)) v
             if (parts == 1) {
                 float f = 1.f, total = ll;
                 if (a.sinks) {
-                    const float sk = a.sinks[hq] * 1.44269504088896341f, top = fmaxf(m, sk);
+                    const float sk = sink_of(a, hq), top = fmaxf(m, sk);
                     f = __builtin_amdgcn_exp2f(m - top);
                     total = ll * f + __builtin_amdgcn_exp2f(sk - top);
                 }

@@ -684,7 +684,8 @@ int32_t qmv_cache_read(const qmv_cache* cache, const int32_t* slots, int64_t n_t
  * only j > p - window.  For query head h, with key/value head
  * h / (n_heads / n_kv_heads):
  *     s_j = scale * q . K_j,   o = sum_j e^(s_j) V_j / (sum_j e^(s_j) + e^(sinks[h])),
- * the last term only where sinks is given.  A query that sees nothing gives 0.
+ * the last term only where sinks is given (+infinity: o = 0; -infinity: none).
+ * A query that sees nothing gives 0.
  *   q          x_type [n_tokens][n_heads][head_dim], strides in elements: per
  *              token any, per head >= head_dim where there is more than one.
  *   n_heads    a multiple of n_kv_heads, at most 1024 * n_kv_heads.
@@ -720,10 +721,11 @@ int32_t qmv_cache_read(const qmv_cache* cache, const int32_t* slots, int64_t n_t
  * that may have more than 32 rows of queries (query tokens times n_heads /
  * n_kv_heads).  fp16 and fp32 queries: two fp16 pieces of each, 22 bits, at
  * twice the arithmetic.  A weight is off by that relative to itself, and by
- * 2^-39 of the row's largest (those 27 nats under it are 0).  |DEQ(K)|
- * and |DEQ(V)| must be within 65024, as qmv_cache_write has them.  A NaN in the cache reaches the queries
- * that see it and no others.  The same call gives the same bits; the other
- * requests' lengths can change the order of a query's sums, nothing else.
+ * 2^-39 of the row's largest (those 27 nats under it are 0).  |DEQ(K)| and
+ * |DEQ(V)| must be within 65024, as qmv_cache_write has them.  A NaN in the
+ * cache reaches the queries that see it and no others.  The same call gives
+ * the same bits; the other requests' lengths can change the order of a query's
+ * sums, nothing else.
  * Errors: QMV_EINVAL, QMV_EALIGN, QMV_EUNSUPPORTED (format), QMV_EHIP.
  */
 size_t qmv_cache_attention_workspace_bytes(const qmv_cache* cache, int64_t n_requests, int64_t n_tokens,

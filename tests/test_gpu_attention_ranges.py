@@ -108,3 +108,23 @@ def test_small_queries_with_a_large_scale(env, x, new, power):
     n = torch.tensor([L], dtype=torch.int32, device="cuda")
     got = qmv.qmv_cache_attention(cache, q * 2.0 ** -power, table, n, scale=2.0 ** power * D ** -0.5)
     ab.close(got, *ab.of_cache(qmv, cache, q, table, [L], [0, new], D ** -0.5, x))
+
+
+@pytest.mark.parametrize("L,new", [(40, 1), (700, 2), (700, 45), (0, 1), (0, 45)])
+@pytest.mark.parametrize("x", ["f32", "f16", "bf16"])
+def test_sinks_without_bound(env, x, L, new):
+    """A sink of +infinity (or past fp32 in units of log 2) leaves nothing for the keys, one of -infinity is none."""
+    torch, qmv = env
+    print(x, L, new, flush=True)
+    H, G, D = 2, 4, 64
+    g = torch.Generator(device="cuda").manual_seed(4)
+    k, v = (torch.randn(max(L, 1), H, D, generator=g, device="cuda") for _ in range(2))
+    cache, table = filled(torch, qmv, k, v, "q4_0", "q8_0")
+    q = torch.randn(new, H * G, D, generator=g, device="cuda").to(getattr(torch, TYPES[x]))
+    n = torch.tensor([L], dtype=torch.int32, device="cuda")
+    inf = float("inf")
+    sinks = torch.tensor([inf, 3.4e38, 3e38, 2e38, -inf, -3.4e38, -3e38, -1e30], device="cuda")
+    got = qmv.qmv_cache_attention(cache, q, table, n, sinks=sinks)
+    plain = qmv.qmv_cache_attention(cache, q, table, n)
+    assert bool((got[:, :4] == 0).all())
+    assert torch.equal(got[:, 4:], plain[:, 4:])
