@@ -454,16 +454,28 @@ __device__ __forceinline__ f16x2 scaled(f16x2 c, f16x2 d, f16x2 m) {
 }
 // What scaled() leaves, as a second fp16 piece.  c d is exact in two pieces;
 // with a minimum, the error of the sum of its first piece and m as well (the
-// six steps are exact).
-template <int F>
+// six steps are exact).  With care also where c d is past fp16 though c d + m
+// is not (a block with values near both ends of the range), which gives NaN
+// without: those steps on halves, and twice their outcome.
+template <int F, bool CARE>
 __device__ __forceinline__ f16x2 scaled_rest(f16x2 c, f16x2 d, f16x2 m, f16x2& first) {
 #pragma clang fp contract(off)
     if constexpr (F == QMV_Q4_1) {      // fused into other multiply-adds these steps would not be exact
+        f16x2 back = h2(1.f);
+        if constexpr (CARE) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const bool wide = __builtin_fabsf((float)d[i]) >= 4096.f;       // 15 * 4096 < 65504
+                d[i] = wide ? d[i] * (_Float16)0.5f : d[i];
+                m[i] = wide ? m[i] * (_Float16)0.5f : m[i];
+                back[i] = wide ? (_Float16)2.f : (_Float16)1.f;
+            }
+        }
         const f16x2 p = c * d, e = __builtin_elementwise_fma(c, d, -p);
         const f16x2 s = p + m, z = s - p;
         const f16x2 rest = (p - (s - z)) + (m - z) + e;
-        first = s;
-        return rest;
+        first = CARE ? s * back : s;
+        return CARE ? rest * back : rest;
     } else {
         first = c * d;
         return __builtin_elementwise_fma(c, d, -first);
@@ -929,7 +941,7 @@ __global__ __launch_bounds__(kAT, (stream_waves<KF, VF, P, NB, NT>())) void attn
                             }
                             if constexpr (!offset) {
                                 c = c - h2(kBase);
-                                if constexpr (P == 2) rest[j] = scaled_rest<VF>(c, vd[j][k], ve[j][k], x[j]);
+                                if constexpr (P == 2) rest[j] = scaled_rest<VF, careful>(c, vd[j][k], ve[j][k], x[j]);
                                 else x[j] = scaled<VF>(c, vd[j][k], ve[j][k]);
                             } else {
                                 x[j] = __builtin_elementwise_fma(c, vd[j][k], ve[j][k]);

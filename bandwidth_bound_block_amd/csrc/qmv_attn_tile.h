@@ -132,7 +132,7 @@ struct TileStep {
                     if constexpr (W8) c = as_h2((__builtin_amdgcn_perm(0, w.w[n][2 * i + j / 2], j & 1 ? 0x0c030c02u : 0x0c010c00u) ^ 0x00800080u) | magic);
                     else c = as_h2(and_or(w.w[n][i] >> (4 * j), mask, magic));
                     c -= bias;
-                    if constexpr (P == 2) rest[j] = scaled_rest<W8 ? QMV_Q8_0 : QMV_Q4_1>(c, d, m, x[j]);
+                    if constexpr (P == 2) rest[j] = scaled_rest<W8 ? QMV_Q8_0 : QMV_Q4_1, CARE>(c, d, m, x[j]);
                     else x[j] = scaled<W8 ? QMV_Q8_0 : QMV_Q4_1>(c, d, m);
                 }
                 uint8_t* to = row + 16 * (4 * b + g);
@@ -222,7 +222,7 @@ struct TileStep {
                     }
                     x[j] -= bias;
                     const f16x2 d = as_h2(j ? d1 : d0), m = as_h2(j ? m1 : m0);
-                    if constexpr (P == 2) rest[j] = scaled_rest<W8 ? QMV_Q8_0 : QMV_Q4_1>(x[j], d, m, y[j]);
+                    if constexpr (P == 2) rest[j] = scaled_rest<W8 ? QMV_Q8_0 : QMV_Q4_1, CARE>(x[j], d, m, y[j]);
                     else y[j] = scaled<W8 ? QMV_Q8_0 : QMV_Q4_1>(x[j], d, m);
                 }
                 *reinterpret_cast<uint2*>(to + e * T::kVRow) = uint2{as_u(y[0]), as_u(y[1])};

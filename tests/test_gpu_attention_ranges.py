@@ -128,3 +128,27 @@ def test_sinks_without_bound(env, x, L, new):
     plain = qmv.qmv_cache_attention(cache, q, table, n)
     assert bool((got[:, :4] == 0).all())
     assert torch.equal(got[:, 4:], plain[:, 4:])
+
+
+@pytest.mark.parametrize("new", [2, 45])
+@pytest.mark.parametrize("kf,vf", [("q4_1", "q4_1"), ("q8_0", "q4_1"), ("q4_1", "q4_0")])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("x", ["f32", "f16", "bf16"])
+def test_blocks_of_both_ends_of_the_range(env, x, D, kf, vf, new):
+    """Q4_1 blocks with values near 65024 of both signs: code times scale is past fp16 though no value is."""
+    torch, qmv = env
+    print(x, D, kf, vf, new, flush=True)
+    H, G, L = 2, 2, 150
+    g = torch.Generator(device="cuda").manual_seed(5)
+    k, v = (torch.randn(L, H, D, generator=g, device="cuda") for _ in range(2))
+    for t, f in ((k, kf), (v, vf)):
+        if f == "q4_1":
+            for j in (0, 17, 60, 149 - new):
+                t[j, j % H, 5:D:32] = 64000.0
+                t[j, j % H, 9:D:32] = -65024.0
+    cache, table = filled(torch, qmv, k, v, kf, vf)
+    assert float(qmv.qmv_cache_read(cache, torch.arange(L, dtype=torch.int32, device="cuda"))[1 if vf == "q4_1" else 0].abs().nan_to_num().max()) > 6e4
+    # queries so small that the large keys have ordinary scores
+    q = ((2e-5 if kf == "q4_1" else 1.0) * torch.randn(new, H * G, D, generator=g, device="cuda")).to(getattr(torch, TYPES[x]))
+    got = qmv.qmv_cache_attention(cache, q, table, torch.tensor([L], dtype=torch.int32, device="cuda"))
+    ab.close(got, *ab.of_cache(qmv, cache, q, table, [L], [0, new], D ** -0.5, x, k_spread=3.0 if kf == "q4_1" else 1.0))
