@@ -15,7 +15,8 @@
 // and values are rounded to fp16 (2^-11; the outputs to 2^-8).  With fp16 or
 // fp32 queries they are pairs of fp16 pieces, fp32 queries too: fp16 outputs
 // had twice the error of their own rounding without.  That costs little here
-// (131000 tokens: 41 us) and twice the time where arithmetic is the bound.
+// (131000 tokens: 41 us, bf16 34) and twice the time where arithmetic is the
+// bound.  Weights go up to 2^14 (kALow), so that small ones keep their digits.
 //
 // The transposition that V needs (a lane multiplies eight keys of one place of
 // the head) happens inside the lane: it loads the same few values of its eight
@@ -43,7 +44,10 @@ constexpr int kAShares = 1024;      // workgroups of the streaming kernel at mos
 constexpr int kABlock = 32;
 // A part of a unit costs its blocks and a beginning and an end (queries, the
 // first loads' latency, the meeting of the waves) of about this many: units
-// count as that much longer, the additional blocks first.
+// count as that much longer, the additional blocks first.  With 4, 8 and 16: 64
+// requests of 200..8000 tokens 73, 64 and 56 us, 200 of 20..500 tokens 57, 52
+// and 50, 16 x 5 fp32 queries 37.2, 35.4 and 34.5, one request of 131000 43, 41
+// and 41; one of 700 the same.
 constexpr int kABegin = 8;
 
 struct AttnArgs {
@@ -490,7 +494,13 @@ __device__ __forceinline__ f16x8 pack8(f16x2 a, f16x2 b, f16x2 c, f16x2 d) {
 // queries leave of the registers, and the rings of LDS.  Three with small
 // heads (64 requests of 200..8000 tokens: 42 us, two 47), two with heads of
 // 128 (one request of 131000 tokens: 38 us, three 50, whose shares are smaller
-// and begin and end more often; 64 requests 65 and 70).
+// and begin and end more often; 64 requests 65 and 70).  One instead of two, by
+// P NT NB = 8: with pairs of pieces it is slower (131000 fp16 49 us for 41, 64
+// requests fp16 115 for 82, 16 x 5 fp32 39.6 for 35.8).  With bf16 queries it
+// would be faster, as two spill registers in the loop over blocks (240 to 630
+// bytes a lane with heads of 128 and two tiles, up to 800 with heads of 256):
+// 64 x 5 queries of four heads 128 us for 133 (Q8_0 135 for 178), 16 x 5 45 for
+// 53, heads of 256 64 requests 79 for 97, one of 131000 57 for 79.
 template <int KF, int VF, int P, int NB, int NT>
 constexpr int stream_waves() {
     constexpr int lds = std::max(2 * Stage<KF, VF, NB>::kBytes, 16 * NT * 68 * 4) * kAWaves + 1024;
@@ -1102,7 +1112,7 @@ __global__ __launch_bounds__(kAT) void attn_join_kernel(const AttnArgs a, int sh
         for (int o = 32; o; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
         f32x4 x = f32x4{0.f, 0.f, 0.f, 0.f};
         float l = 0.f;
-        // eight parts' loads at a time: one by one 128 parts of a row took 9.1 us, most of it waiting, now 6.3
+        // eight parts' loads at a time: one by one 128 parts of a row took 9.1 us, most of it waiting, now 5.9
         constexpr int kLoads = 8;
         for (int64_t s = s0 + part; s <= s1; s += kLoads * kPer) {
             float mm[kLoads], ll[kLoads];

@@ -17,10 +17,21 @@ size_t stream_bytes(const qmv_cache& c, int64_t R, int32_t heads, int64_t max_q)
     return round16((size_t)(R + 2) * 8) + (size_t)(2 * kAShares * rows * (c.head_dim + 2)) * 4;
 }
 
-// Rows of a request up to which the streaming kernel takes it.
+// Rows of a request up to which the streaming kernel takes it.  Requests behind
+// 900..4000 tokens, 8 key/value heads of 128, 8 query heads each, streaming and
+// tile kernel: of 24 rows 16 requests 54 and 109 us, 64 142 and 240; of 32 rows 57 and
+// 110, 149 and 230; of 40 rows 82 and 97, 254 and 230; of 64 rows 84 and 95,
+// 258 and 228; of 128 rows 138 and 93, 479 and 232.  One request behind 8000, 4
+// query heads each: 24 rows 30 and 26, 40 rows 35 and 28.  fp16 queries would
+// go further: 40 rows 92 and 202, 307 and 542; 64 rows 95 and 194, 319 and 539;
+// 128 rows 167 and 194, 612 and 581.
 constexpr int kFewRows = 32;
 // Parts that the tile kernel's tiles are split into over the keys, where there
-// are fewer tiles than the GPU runs at once.
+// are fewer tiles than the GPU runs at once: a workgroup for each of 256 compute
+// units.  With half as many, 200 tokens behind 8000 take 101 us for 68, 512
+// behind 4000 102 for 69; small mixed steps less (54 us, 52).  At most 32: with 16,
+// 64 tokens behind 30000 take 96 us for 68, with both limits many short ones
+// the same (5 x 123 tokens 29 us, 29).
 int tile_splits(const qmv_cache& c, int64_t T, int32_t heads, int64_t max_q, int32_t x_type) {
     const int64_t G = heads / c.n_kv_heads;
     if (max_q * G <= kFewRows) return 0;

@@ -14,11 +14,11 @@
 // the first group the keys', the second the values'.  All waves in step left
 // the matrix and the vector pipes waiting for each other: 458 us against 386
 // for 2048 bf16 queries behind 6144 keys, 32 heads of 128, Q4_0.  That is
-// 622 TF/s (324 us, 742, where calls follow each other); what bounds it is the vector work beside the products (exponentials
-// and their scales, codes to values), about as long as they are.  Codes are on
-// their way two phases before they are used.  fp16 and fp32 queries (P 2) take
-// three products for one, 760..820 us.  Few tiles are split over the keys and
-// joined by a second launch.
+// 622 TF/s (327 us, 735, where calls follow each other); what bounds it is the
+// vector work beside the products (exponentials and their scales, codes to
+// values), about as long as they are.  Codes are on their way two phases before
+// they are used.  fp16 and fp32 queries (P 2) take three products for one,
+// 720..790 us.  Few tiles are split over the keys and joined by a second launch.
 #pragma once
 #include "qmv_attention.h"
 
@@ -257,7 +257,7 @@ __device__ __forceinline__ void products(const Read& read, const Multiply& multi
 
 // Parts that a request's tiles are split into: no more than leave four blocks
 // of 32 keys to each.  A part that has less costs more than it takes over: 123
-// tokens of 5 requests, none before them, took 61 us in 10 parts each, now 41.
+// tokens of 5 requests, none before them, took 61 us in 10 parts each, now 39.
 __device__ __forceinline__ int parts_of(const Req& rq, int splits) { return min(splits, max(1, rq.nblk / 4)); }
 
 template <int D, int P, bool K8, bool V8>

@@ -2,7 +2,7 @@
 //
 // A thread has an octet of a token's head: four neighbouring threads share a
 // block of 32 values and its scale.  Both are bound by memory (a write of 6000
-// tokens of 8 heads of 128 from fp32, 60 MB, takes 17 us) and, for a few tokens,
+// tokens of 8 heads of 128 from fp32, 60 MB, takes 18 us) and, for a few tokens,
 // by the launch (48 tokens 5 us, 333 read 3 us).
 #include <algorithm>
 
@@ -60,7 +60,8 @@ __device__ __forceinline__ float quad_xor(float v) {
 // fp32 quotient is at most 2^-14 off where the code is within its range, so
 // only next to a border between two codes is the fp64 one needed (its
 // rounding, 2^-53, is less than any quotient's distance from a border that it
-// is not on: w and d together have 35 bits).
+// is not on: w and d together have 35 bits; with a minimum the difference of w
+// and m is rounded to fp64 first).
 __device__ __forceinline__ void codes_of(const float (&w)[8], float d, float m, float lo, float hi, int (&c)[8]) {
     const float inv = 1.f / d;
     bool near = false;
@@ -292,7 +293,9 @@ dim3 cache_grid(const CacheArgs& a) {
 // Heads of a thread of the read, which shares the slot's page and the addresses
 // between them: four once two workgroups for each compute unit are left.  65536
 // tokens of 8 heads of 128: 72 us (344 MB, 4.8 TB/s, what a copy reaches), one
-// head a thread 126; 6000 tokens to fp32 14.2 and 16.3.
+// head a thread 126; 32000 30.0 and 31.6.  To fp32 6000 tokens of Q8_0 and Q4_1
+// 14.2 and 16.3, but of Q4_0 8000 21.7 and 17.9, 32000 80 and 77.  Under the
+// border (2048 tokens of 8 heads) both are the launch.
 constexpr int kReadHeads = 4;
 template <class XT>
 void launch_read(const CacheArgs& a, hipStream_t st) {

@@ -13,9 +13,9 @@
 // maximum reaches it have candidates, whose logits the second launch reads
 // again; places among the candidates are counted.  Candidates found in the
 // first launch (ballots and a sort of lanes' maxima in every chunk) took 299
-// us for 500 x 151936, where the two launches now take 31 us (152 MB at 4.9
-// TB/s, with 88% of the vector issue slots taken) and 13 us (reads
-// that wait for one another); one row of 128256 takes 4.5 and 7 us.
+// us for 500 x 151936, where the two launches now take 33 us (152 MB at 4.6
+// TB/s, with 82% of the vector issue slots taken) and 15 us (reads that wait
+// for one another), together 43; one row of 128256 takes 4 and 7 us.
 #include <algorithm>
 #include <type_traits>
 
@@ -33,9 +33,17 @@ constexpr int kLWaves = kLT / 64;
 // bf16 logits, with 16 a thread 32.6; for one row of 128256 4.5 and 3.9, with
 // 64 it was 5.9.
 constexpr int kLPer = 32;
-constexpr int kLGroup = 64;                   // logits of a group: those of kLGroup / kLPer threads
+// Logits of a group: those of kLGroup / kLPer threads.  With 32, 64 and 128: 500
+// rows of 151936, top 20, 44.2, 43.2 and 44.7 us, 500 of 32000 22.7, 22.6 and 24.3.
+constexpr int kLGroup = 64;
 constexpr int kLTop = 32;
-constexpr int kLCands = 1024;                 // groups that reach the bound, and candidates, of a row that LDS holds
+// Groups that reach the bound, and candidates, of a row that LDS holds, in 12
+// KB (registers, not these, bound the workgroups of a compute unit).  A row with
+// more (many equal logits, or fewer tokens than top_k beside a finite mask) is
+// scanned once for each of its top tokens: 500 rows of 151936 with 8 tokens,
+// the rest at the type's lowest value, take 4140 us for the top 20, 41 for the
+// top 5; with -infinity in their place 39.
+constexpr int kLCands = 1024;
 constexpr int kLKeep = 16;                    // maxima of groups that a thread keeps in registers
 
 struct ChunkStat {

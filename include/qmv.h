@@ -646,7 +646,7 @@ size_t qmv_cache_page_bytes(qmv_fmt fmt, int32_t n_kv_heads, int32_t head_dim, i
  *     Q4_1  m = fp16(min), d = fp16((max - min) / 15),
  *                                        c = round((w - m) / d) in 0..15
  * with the quotient of d rounded to fp32 before it is rounded to fp16, and
- * the codes those of the exact w / d.  d = 0 (never -0) gives codes that
+ * the codes those of the exact w / d (Q4_1: of w - m in fp64).  d = 0 (never -0) gives codes that
  * stand for 0 (m).  Values past +-65024 are stored as that (what DEQ gives then stays
  * within fp16); a block with a NaN or an infinity reads back as NaN.
  *   k, v      x_type (QMV_X_F32, QMV_X_F16, QMV_X_BF16) [n_tokens]
@@ -714,18 +714,18 @@ int32_t qmv_cache_read(const qmv_cache* cache, const int32_t* slots, int64_t n_t
  *              2^31;  max_pages >= 1, with max_pages * page_size <= 2^30.
  * Nothing is read back to the host: a captured call may be replayed with
  * other lengths, tables and q_begin (within max_q).
- * Statistics and sums are fp32.  bf16 queries: codes are exact in the matrix
- * cores' fp16, queries are scaled by a power of two per row to fp16 (exact
- * for all elements within 2^-27 of the row's largest), weights and DEQ(V) are
- * rounded to fp16, and so is DEQ(K) for a request, or a call of one request,
- * that may have more than 32 rows of queries (query tokens times n_heads /
- * n_kv_heads).  fp16 and fp32 queries: two fp16 pieces of each, 22 bits, at
- * twice the arithmetic.  A weight is off by that relative to itself, and by
- * 2^-39 of the row's largest (those 27 nats under it are 0).  |DEQ(K)| and
- * |DEQ(V)| must be within 65024, as qmv_cache_write has them.  A NaN in the
- * cache reaches the queries that see it and no others.  The same call gives
- * the same bits; the other requests' lengths can change the order of a query's
- * sums, nothing else.
+ * Statistics and sums are fp32.  bf16 queries: codes are exact in fp16 (below
+ * its normal numbers, whose products the matrix cores take to about 2^-20),
+ * queries are scaled by a power of two per row to fp16 (exact for all elements
+ * within 2^-27 of the row's largest), weights and DEQ(V) are rounded to fp16,
+ * and so is DEQ(K) for a request, or a call of one request, that may have more
+ * than 32 rows of queries (query tokens times n_heads / n_kv_heads).  fp16 and fp32 queries: two fp16 pieces of each, 22 bits, at
+ * twice the arithmetic (elements of queries to 2^-35 of their row's largest).
+ * A weight is off by that relative to itself, and by 2^-39 of the row's
+ * largest (those 27 nats under it are 0).  |DEQ(K)| and |DEQ(V)| must be within
+ * 65024, as qmv_cache_write has them.  A NaN in the cache reaches the queries
+ * that see it and no others.  The same call gives the same bits; the other
+ * requests' lengths can change the order of a query's sums, nothing else.
  * Errors: QMV_EINVAL, QMV_EALIGN, QMV_EUNSUPPORTED (format), QMV_EHIP.
  */
 size_t qmv_cache_attention_workspace_bytes(const qmv_cache* cache, int64_t n_requests, int64_t n_tokens,
