@@ -101,3 +101,81 @@ def test_more_tiles_than_workgroups(env, x, D):
         rows = slice(int(begin[r]), int(begin[r + 1]))
         want, bound = ab.of_cache(qmv, cache, q[rows], table[r:r + 1], n[r:r + 1].tolist(), [0, 1], D ** -0.5, x)
         ab.close(got[rows], want, bound)
+
+
+@pytest.mark.parametrize("x", ["f32", "bf16"])
+@pytest.mark.parametrize("G,most", [(2, 90), (4, 8), (64, 3)])
+def test_replayed_with_other_requests(env, G, most, x):
+    """q_begin, lengths and tables change between replays of one graph, and with them which kernel has a request."""
+    torch, qmv = env
+    print(G, most, x, flush=True)
+    g = torch.Generator(device="cuda").manual_seed(11)
+    rng = np.random.default_rng(most)
+    H, D, P, R, T = 2, 64, 16, 6, 3 * most
+    cache, full = random_cache(torch, qmv, g, "q8_0", "q4_0", H, D, P, [900] * R)
+    q = torch.randn(T, H * G, D, generator=g, device="cuda").to(getattr(torch, TYPES[x]))
+    table, n = full.clone(), torch.full((R,), 40, dtype=torch.int32, device="cuda")
+    begin = torch.zeros(R + 1, dtype=torch.int32, device="cuda")
+    out = torch.zeros_like(q)
+    ws = torch.empty(qmv.lib().qmv_cache_attention_workspace_bytes(cache._struct, R, T, H * G, most), dtype=torch.uint8, device="cuda")
+
+    def call(to, workspace):
+        return qmv.qmv_cache_attention(cache, q, table, n, begin, most, window=500, out=to, workspace=workspace)
+    call(out, ws)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(out, ws)
+    for i in range(8):
+        new = rng.integers(0, most + 1, R) * rng.integers(0, 2, R) if i else np.zeros(R, int)
+        while new.sum() > T:
+            new[rng.integers(R)] = rng.integers(0, 2)
+        at = np.concatenate([[0], np.cumsum(new)])
+        lens = np.maximum(rng.integers(1, 900, R), new)
+        begin.copy_(torch.from_numpy(at.astype(np.int32)))
+        n.copy_(torch.from_numpy(lens.astype(np.int32)))
+        table.copy_(full[torch.randperm(R, generator=g, device="cuda")])
+        q.normal_(generator=g)
+        out.fill_(7.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert bool((out[at[-1]:] == 7).all())
+        assert torch.equal(out, call(torch.full_like(out, 7.0), None)), i
+        if at[-1]:
+            want, bound = ab.of_cache(qmv, cache, q, table, lens, at, D ** -0.5, x, 500)
+            ab.close(out[:at[-1]], want[:at[-1]], bound[:at[-1]])
+        torch.randn(5000, device="cuda").sum()
+
+
+@pytest.mark.parametrize("x,new", [("bf16", 1), ("f32", 2), ("bf16", 40)])
+def test_millions_of_keys(env, x, new):
+    """One request whose weights are all alike in size: sums of 3 million of them."""
+    torch, qmv = env
+    L, D, P = 3_000_001, 64, 4096
+    print(x, new, L, flush=True)
+    g = torch.Generator(device="cuda").manual_seed(13)
+    pages = -(-L // P)
+    cache = qmv.KVCache.new(pages, "q4_0", "q8_0", 1, D, P)
+    table = torch.randperm(pages, generator=g, device="cuda").to(torch.int32)
+    for c in range(0, L, 1 << 18):
+        j = torch.arange(c, min(c + (1 << 18), L), device="cuda")
+        k = torch.randn(j.numel(), 1, D, generator=g, device="cuda")
+        v = 1.0 + torch.randn(j.numel(), 1, D, generator=g, device="cuda")
+        qmv.qmv_cache_write(cache, k, v, (table[j // P] * P + j % P).to(torch.int32))
+    q = torch.randn(new, 1, D, generator=g, device="cuda").to(getattr(torch, TYPES[x]))
+    n = torch.tensor([L], dtype=torch.int32, device="cuda")
+    got = qmv.qmv_cache_attention(cache, q, table.view(1, -1), n)
+    total, out = torch.zeros(new, 1, dtype=torch.float64, device="cuda"), torch.zeros(new, D, dtype=torch.float64, device="cuda")
+    pos = torch.arange(L - new, L, device="cuda")[:, None]
+    for c in range(0, L, 1 << 18):
+        j = torch.arange(c, min(c + (1 << 18), L), device="cuda")
+        k, v = (t[:, 0].double() for t in qmv.qmv_cache_read(cache, (table[j // P] * P + j % P).to(torch.int32)))
+        w = torch.exp(torch.matmul(q[:, 0].double(), k.t().contiguous()) * D ** -0.5).masked_fill(j > pos, 0.0)
+        total += w.sum(1, keepdim=True)
+        out += torch.matmul(w, v)
+    want = (out / total)[:, None]
+    # outputs are means of values about 1, of roundings of random signs but for those of the sums: a wave adds some 1500 (two
+    # rounds of 32 keys) or, in the kernel for many rows, 3000 times at most, each 2^-24 of a part of the sum
+    off = float((got.double() - want).abs().max())
+    print("off", off, flush=True)
+    assert off <= ab.HALF[x] * 1.5 + (2 * ab.H16 if x == "bf16" else 0) + 6000 * ab.U
